@@ -60,6 +60,8 @@ typedef int32_t isd_status;
 #define ISD_FLAG_NCLEAN_RANGE  4  /* n_clean outside [1, N] */
 #define ISD_FLAG_CAPACITY      8  /* kv_len + block exceeds the request's page capacity */
 #define ISD_FLAG_WAIT_TIMEOUT 16  /* a bounded on-chip wait gave up (LM-head pipeline) */
+#define ISD_FLAG_CHUNK_RANGE  32  /* q_start does not ascend within [0, T] */
+#define ISD_FLAG_PARENT_OOB   64  /* a parent outside [-1, B) */
 
 #define ISD_PROPOSE_ARGMAX 0      /* argmax proposals ([ENG §服务部署与 SGLang 集成]) */
 #define ISD_PROPOSE_SAMPLE 1      /* inverse-CDF draws with the u_prop uniforms */
@@ -498,6 +500,117 @@ isd_status isd_layers(const isd_dims* d, int32_t n_layers, int32_t inter, float 
                       const uint16_t* final_norm, uint16_t* x, uint16_t* out,
                       const int32_t* page_table, const int32_t* kv_len, const int32_t* n_clean,
                       void* ws, size_t ws_bytes, int32_t* err_flag, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Prompts and pages.  The pages the block attention reads have to be filled
+ * with prompts first, and given back when an answer ends; the I-DLM pages
+ * leave both to the AR serving stack ([EXP §推理：复用 AR 推理栈]: paged KV
+ * cache, chunked prompts).
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * isd_chunk_attention -- KV append + causal GQA attention of a chunk of new
+ * tokens per request over the paged cache: prompts, in one piece or several,
+ * and plain decoding (one token per request), mixed in one call.
+ *   T      rows of q, k_new, v_new and out
+ *   q      [T, Hq, D] bf16; k_new, v_new [T, Hkv, D] bf16
+ *   q_start [B+1] int32, ascending within [0, T]: rows q_start[b] ..
+ *          q_start[b+1]-1 are request b's new tokens (none is allowed), at
+ *          positions kv_len[b], kv_len[b]+1, ...
+ *   k_pool, v_pool, page_table, kv_len: as for isd_attention; the new tokens'
+ *          K/V rows are written at their positions, no other row is.  The
+ *          page list must cover kv_len[b] + the new tokens (isd_fork_requests
+ *          makes room); kv_len itself is the caller's to advance.
+ *   out    [T, Hq*D] bf16: row i, head h: the softmax (sm_scale q.k) weighted
+ *          sum of v over the request's keys at positions <= the row's, query
+ *          head h reading KV head h / (Hq/Hkv).  Rows of no request are not
+ *          written.
+ * What a cache row at or past a request's last position holds is not read
+ * into any result (it may be NaN); nor is a key or value that a row's causal
+ * mask hides.
+ * Supported: D in {64, 128}, Hq/Hkv <= 128.  N and V of the dims are not used
+ * (any positive values).  Workspace: isd_chunk_workspace_bytes(d, T) bytes,
+ * 256-aligned (0 for invalid dims or T < 0); one made for a larger T serves.
+ * Errors: a null pointer, invalid dims, T < 0 or an sm_scale that is not
+ * positive and finite -> ISD_ERR_INVALID_ARG (a tensor not 16-byte aligned too); a shape not supported ->
+ * ISD_ERR_UNSUPPORTED_SHAPE; a workspace too small or misaligned ->
+ * ISD_ERR_WORKSPACE.  On the device: ISD_FLAG_CHUNK_RANGE (no request is
+ * served); ISD_FLAG_CAPACITY (a request with a negative kv_len or tokens past
+ * its pages: its rows of out are zero, its cache is left alone);
+ * ISD_FLAG_PAGE_OOB (keys and values on a page id outside the pool read as
+ * zeros, and are not written).  Two calls may overlap on the GPU if their
+ * workspaces and the cache rows they write differ.
+ */
+size_t isd_chunk_workspace_bytes(const isd_dims* d, int32_t T);
+isd_status isd_chunk_attention(const isd_dims* d, int32_t T, const uint16_t* q,
+                               const uint16_t* k_new, const uint16_t* v_new, uint16_t* k_pool,
+                               uint16_t* v_pool, const int32_t* page_table, const int32_t* kv_len,
+                               const int32_t* q_start, uint16_t* out, void* ws, size_t ws_bytes,
+                               int32_t* err_flag, void* stream);
+
+/*
+ * isd_fork_requests -- the next batch made of this one: slot r of the new
+ * batch of R slots continues request parent[r] (-1: an empty slot).  A
+ * request that no slot names is dropped; one that several name is forked; the
+ * same call moves requests between slots and makes room for their next tokens.
+ *   parent [R] int32; reserve [R] int32 or NULL (0): tokens to make room for
+ *   kv_len, pages_used [B], page_table [B, max_pages_per_req],
+ *   next_free_page [1] int32: this batch's state (isd_prepare_block's)
+ *   pools  HOST array of n_pools device pointers, each [num_pages, page_size,
+ *          Hkv, D] bf16: every layer's k_pool and v_pool
+ * Outputs (int32; none may overlap an input): next_kv_len, next_pages_used
+ * [R], next_page_table [R, max_pages_per_req] (-1 past pages_used),
+ * next_free_out [1].
+ *  - The first slot that names a request keeps its page list; each further one
+ *    shares the pages that are full (kv_len / P of them; no later step writes
+ *    there) and gets its own copy of the rows of the part-filled page.
+ *  - Page lists are then extended to ceil((kv_len + reserve) / P) pages.  New
+ *    pages come in slot order from *next_free_page on.
+ *  - Of the pools, only pages from *next_free_page on are written.  Nothing of
+ *    the old batch's state changes: the call can be repeated, or the new state
+ *    be thrown away.
+ * Supported: page bytes (Hkv * D * 2 per token) a multiple of 16; B <= 12000.
+ * N, V, Hq and sm_scale are not used.
+ * Errors: invalid dims, R < 1, n_pools < 0, a null or misaligned pointer, an
+ * output that is also an input -> ISD_ERR_INVALID_ARG; else
+ * ISD_ERR_UNSUPPORTED_SHAPE.  On the device a slot that cannot be made is left
+ * empty (length 0, no pages): ISD_FLAG_PARENT_OOB, or ISD_FLAG_CAPACITY (page
+ * list longer than the table or than the pool has left, in slot order; a
+ * negative length, page count or reserve; fewer pages than kv_len needs).
+ * ISD_FLAG_PAGE_OOB: a page id outside the pool is passed on, not copied.
+ */
+isd_status isd_fork_requests(const isd_dims* d, int32_t R, const int32_t* parent,
+                             const int32_t* reserve, const int32_t* kv_len,
+                             const int32_t* pages_used, const int32_t* page_table,
+                             const int32_t* next_free_page, int32_t n_pools,
+                             uint16_t* const* pools, int32_t* next_kv_len,
+                             int32_t* next_pages_used, int32_t* next_page_table,
+                             int32_t* next_free_out, int32_t* err_flag, void* stream);
+
+/*
+ * isd_compact_pages -- the pages still in use (named by the first
+ * pages_used[b] columns of some request b) become pages 0 .. L-1, so that the
+ * bump allocator can hand out L .. num_pages-1 again.  A used page before L
+ * stays; the k-th used page from L on moves to the k-th unused place before L.
+ *   pages_used [B], page_table [B, max_pages_per_req] int32; pools as above
+ *   (every pool moves the same pages)
+ *   next_page_table [B, max_pages_per_req] int32 (may be page_table itself):
+ *          the table after the move, -1 past pages_used; next_free_out [1] = L
+ * A page that several requests share moves once.  Pages from L on keep their
+ * bytes, so the call can be repeated on the same inputs.
+ * Workspace: isd_pages_workspace_bytes(d) bytes, 256-aligned.  Supported as
+ * isd_fork_requests (any B).  Errors as there; a workspace too small or
+ * misaligned -> ISD_ERR_WORKSPACE.  On the device: ISD_FLAG_PAGE_OOB (the
+ * entry is passed on), ISD_FLAG_CAPACITY (a pages_used outside
+ * [0, max_pages_per_req] counts as the nearest bound).
+ */
+size_t isd_pages_workspace_bytes(const isd_dims* d);
+isd_status isd_compact_pages(const isd_dims* d, const int32_t* pages_used,
+                             const int32_t* page_table, int32_t n_pools, uint16_t* const* pools,
+                             int32_t* next_page_table, int32_t* next_free_out, void* ws,
+                             size_t ws_bytes, int32_t* err_flag, void* stream);
 
 #ifdef __cplusplus
 }

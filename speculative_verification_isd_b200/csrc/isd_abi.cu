@@ -5,6 +5,7 @@
 // isd_layers call for a new projection shape times cuBLASLt's candidate
 // algorithms on its stream (outside stream capture only).
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <stdio.h>
 
@@ -75,6 +76,19 @@ cudaError_t launch_sdar_unmask(const isd_dims* d, float tau, bool sync, const fl
                                int32_t* block_tok, int32_t* steps, int32_t* kv_len,
                                int32_t* unmasked, int32_t* out_tok, int32_t* block_steps,
                                int* counters, int32_t* err_flag, cudaStream_t st, bool pdl);
+cudaError_t launch_chunk_attention(const isd_dims* d, int T, const uint16_t* q, const uint16_t* k_new,
+                                   const uint16_t* v_new, uint16_t* k_pool, uint16_t* v_pool,
+                                   const int32_t* page_table, const int32_t* kv_len,
+                                   const int32_t* q_start, uint16_t* out, void* ws, int32_t* err_flag,
+                                   cudaStream_t st);
+cudaError_t launch_fork(const isd_dims* d, int R, const int32_t* parent, const int32_t* reserve,
+                        const int32_t* kv_len, const int32_t* pages_used, const int32_t* page_table,
+                        const int32_t* next_free, int n_pools, uint16_t* const* pools,
+                        int32_t* next_kv_len, int32_t* next_pages_used, int32_t* next_table,
+                        int32_t* next_free_out, int32_t* err_flag, cudaStream_t st);
+cudaError_t launch_compact(const isd_dims* d, const int32_t* pages_used, const int32_t* page_table,
+                           int n_pools, uint16_t* const* pools, int32_t* next_table,
+                           int32_t* next_free_out, void* ws, int32_t* err_flag, cudaStream_t st);
 cudaError_t launch_accept(const Plan& p, const isd_dims* d, const float* logits,
                           const isd_row_stat* stats, const float* prev_logits,
                           const isd_row_stat* prev_stats, const int32_t* n_clean,
@@ -673,6 +687,124 @@ isd_status isd_layers(const isd_dims* d, int32_t n_layers, int32_t inter, float 
         ISD_CUDA(gemm(H, inter, act, L.w_down, x, true));
     }
     if (final_norm) ISD_CUDA(isd::launch_rmsnorm(x, final_norm, out, M, H, eps, st));
+    return ISD_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Prompts and pages (chunk.cu, pages.cu).
+// ---------------------------------------------------------------------------
+namespace {
+
+bool cache_dims_ok(const isd_dims* d) {
+    return d && d->B >= 1 && d->Hkv >= 1 && d->D >= 1 && d->page_size >= 1 && d->num_pages >= 1 &&
+           d->max_pages_per_req >= 1;
+}
+
+bool chunk_dims_ok(const isd_dims* d) {
+    return cache_dims_ok(d) && d->Hq >= 1 && d->Hq % d->Hkv == 0 && d->N >= 1 && d->V >= 1;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+isd_status check_ws_bytes(size_t need, void* ws, size_t ws_bytes) {
+    if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255)) {
+        snprintf(g_last_error, sizeof(g_last_error), "workspace: need %zu bytes, 256-aligned", need);
+        return ISD_ERR_WORKSPACE;
+    }
+    return ISD_OK;
+}
+
+isd_status check_pools(const isd_dims* d, int32_t n_pools, uint16_t* const* pools) {
+    if (n_pools < 0 || (n_pools > 0 && !pools)) return invalid("pools");
+    for (int32_t i = 0; i < n_pools; ++i)
+        if (!pools[i] || !aligned16(pools[i])) return invalid("a pool is null or not 16-byte aligned");
+    if ((size_t)d->Hkv * d->D * 2 % 16) return unsupported("a token's K row must be a multiple of 16 bytes");
+    return ISD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t isd_chunk_workspace_bytes(const isd_dims* d, int32_t T) {
+    if (!chunk_dims_ok(d) || T < 0) return 0;
+    return isd::chunk_ws_bytes(d, T);
+}
+
+isd_status isd_chunk_attention(const isd_dims* d, int32_t T, const uint16_t* q,
+                               const uint16_t* k_new, const uint16_t* v_new, uint16_t* k_pool,
+                               uint16_t* v_pool, const int32_t* page_table, const int32_t* kv_len,
+                               const int32_t* q_start, uint16_t* out, void* ws, size_t ws_bytes,
+                               int32_t* err_flag, void* stream) {
+    if (!chunk_dims_ok(d)) return invalid("dims");
+    if (T < 0) return invalid("T < 0");
+    ISD_TRY(check_ws_bytes(isd::chunk_ws_bytes(d, T), ws, ws_bytes));
+    if (!k_pool || !v_pool || !page_table || !kv_len || !q_start ||
+        (T > 0 && (!q || !k_new || !v_new || !out)))
+        return invalid("null chunk-attention pointer");
+    if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) ||
+        !aligned16(v_pool) || !aligned16(out))
+        return invalid("a chunk-attention tensor is not 16-byte aligned");
+    if (!(d->sm_scale > 0.f && d->sm_scale < INFINITY)) return invalid("sm_scale must be positive and finite");
+    if (d->D != 64 && d->D != 128) return unsupported("head dim must be 64 or 128");
+    if (d->Hq / d->Hkv > 128) return unsupported("Hq/Hkv must be <= 128");
+    if (T == 0) return ISD_OK;
+    ISD_CUDA(isd::launch_chunk_attention(d, T, q, k_new, v_new, k_pool, v_pool, page_table, kv_len,
+                                         q_start, out, ws, err_flag, static_cast<cudaStream_t>(stream)));
+    return ISD_OK;
+}
+
+isd_status isd_fork_requests(const isd_dims* d, int32_t R, const int32_t* parent,
+                             const int32_t* reserve, const int32_t* kv_len,
+                             const int32_t* pages_used, const int32_t* page_table,
+                             const int32_t* next_free_page, int32_t n_pools,
+                             uint16_t* const* pools, int32_t* next_kv_len,
+                             int32_t* next_pages_used, int32_t* next_page_table,
+                             int32_t* next_free_out, int32_t* err_flag, void* stream) {
+    if (!cache_dims_ok(d)) return invalid("dims");
+    if (R < 1) return invalid("R < 1");
+    if (!parent || !kv_len || !pages_used || !page_table || !next_free_page || !next_kv_len ||
+        !next_pages_used || !next_page_table || !next_free_out)
+        return invalid("null fork pointer");
+    ISD_TRY(check_pools(d, n_pools, pools));
+    if (d->B > 12000) return unsupported("B must be <= 12000");
+    const size_t cols = (size_t)d->max_pages_per_req * 4, b4 = (size_t)d->B * 4, r4 = (size_t)R * 4;
+    const void* in[6] = {parent, reserve, kv_len, pages_used, page_table, next_free_page};
+    const size_t in_n[6] = {r4, reserve ? r4 : 0, b4, b4, d->B * cols, 4};
+    const void* outs[4] = {next_kv_len, next_pages_used, next_page_table, next_free_out};
+    const size_t out_n[4] = {r4, r4, R * cols, 4};
+    for (int o = 0; o < 4; ++o)
+        for (int i = 0; i < 6; ++i)
+            if (in_n[i] && overlaps(outs[o], out_n[o], in[i], in_n[i]))
+                return invalid("a fork output overlaps an input");
+    ISD_CUDA(isd::launch_fork(d, R, parent, reserve, kv_len, pages_used, page_table, next_free_page,
+                              n_pools, pools, next_kv_len, next_pages_used, next_page_table,
+                              next_free_out, err_flag, static_cast<cudaStream_t>(stream)));
+    return ISD_OK;
+}
+
+size_t isd_pages_workspace_bytes(const isd_dims* d) {
+    return cache_dims_ok(d) ? isd::pages_ws_bytes(d) : 0;
+}
+
+isd_status isd_compact_pages(const isd_dims* d, const int32_t* pages_used,
+                             const int32_t* page_table, int32_t n_pools, uint16_t* const* pools,
+                             int32_t* next_page_table, int32_t* next_free_out, void* ws,
+                             size_t ws_bytes, int32_t* err_flag, void* stream) {
+    if (!cache_dims_ok(d)) return invalid("dims");
+    ISD_TRY(check_ws_bytes(isd::pages_ws_bytes(d), ws, ws_bytes));
+    if (!pages_used || !page_table || !next_page_table || !next_free_out)
+        return invalid("null compact pointer");
+    ISD_TRY(check_pools(d, n_pools, pools));
+    ISD_CUDA(isd::launch_compact(d, pages_used, page_table, n_pools, pools, next_page_table,
+                                 next_free_out, ws, err_flag, static_cast<cudaStream_t>(stream)));
     return ISD_OK;
 }
 

@@ -1,0 +1,371 @@
+// Page bookkeeping of the paged KV cache between steps: a new batch made of
+// an old one (requests continued, forked, moved to other slots or dropped),
+// and compaction, which gives the bump allocator the dropped pages back.
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "plan.h"
+
+namespace isd {
+
+namespace {
+
+constexpr int kPageThreads = 256;
+
+struct ForkArgs {
+    int B, R, P, num_pages, max_pages, n_pools;
+    size_t row_bytes, page_bytes;  // one token's K (or V) rows; one page of a pool
+    const int32_t* parent;
+    const int32_t* reserve;  // or null: no room asked for
+    const int32_t* kv_len;
+    const int32_t* pages_used;
+    const int32_t* page_table;
+    const int32_t* next_free;
+    int32_t* next_kv_len;
+    int32_t* next_pages_used;
+    int32_t* next_table;
+    int32_t* next_free_out;
+    int32_t* err_flag;
+};
+
+// What child r takes over: `have` columns of its parent's row, `need` columns
+// in all (need - have new pages), and whether it is the parent's first child.
+struct Child {
+    int par, kv, have, need;
+    bool first;
+    int fault;  // an ISD_FLAG_* bit: the slot is left empty
+};
+
+ISD_DEVINL Child child_of(const ForkArgs& a, const int* first_of, int r) {
+    Child c = {-1, 0, 0, 0, false, 0};
+    const int par = a.parent[r];
+    if (par == -1) return c;
+    if (par < 0 || par >= a.B) {
+        c.fault = ISD_FLAG_PARENT_OOB;
+        return c;
+    }
+    const int kv = a.kv_len[par], used = a.pages_used[par];
+    const int more = a.reserve ? a.reserve[r] : 0;
+    const bool first = first_of[par] == r;
+    const long long want = ((long long)kv + more + a.P - 1) / a.P;
+    const int whole = kv / a.P, cover = (int)(((long long)kv + a.P - 1) / a.P);
+    if (kv < 0 || more < 0 || used < cover || used > a.max_pages || want > a.max_pages) {
+        c.fault = ISD_FLAG_CAPACITY;
+        return c;
+    }
+    c.par = par;
+    c.kv = kv;
+    c.first = first;
+    c.have = first ? used : whole;
+    c.need = max((int)want, first ? used : cover);
+    return c;
+}
+
+template <typename T>
+ISD_DEVINL T block_sum(T v, T* part) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    T t = 0;
+    for (int i = 0; i < kPageThreads / 32; ++i) t += part[i];
+    __syncthreads();
+    return t;
+}
+
+// grid (R, pieces of the pools): every CTA works out its child's new pages
+// (the counts of the children before it, in slot order), the first piece
+// writes the child's state, and all copy the part-filled last page.
+__global__ void __launch_bounds__(kPageThreads) fork_kernel(const __grid_constant__ ForkArgs a,
+                                                            const __grid_constant__ PoolList pools) {
+    extern __shared__ int first_of[];  // [B]: the first child of each request
+    __shared__ long long part[kPageThreads / 32];
+    const int r = blockIdx.x;
+    for (int b = threadIdx.x; b < a.B; b += kPageThreads) first_of[b] = a.R;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.R; i += kPageThreads) {
+        const int p = a.parent[i];
+        if (p >= 0 && p < a.B) atomicMin(&first_of[p], i);
+    }
+    __syncthreads();
+    long long before = 0;
+    for (int i = threadIdx.x; i < r; i += kPageThreads) {
+        const Child c = child_of(a, first_of, i);
+        before += c.need - c.have;
+    }
+    before = block_sum(before, part);
+    Child c = child_of(a, first_of, r);
+    const long long free0 = max(*a.next_free, 0);
+    const long long base = free0 + before;
+    if (c.need > c.have && base + (c.need - c.have) > a.num_pages) {
+        c = Child{-1, 0, 0, 0, false, ISD_FLAG_CAPACITY};
+    }
+    if (blockIdx.y == 0) {
+        if (threadIdx.x == 0) {
+            if (c.fault) raise_flag(a.err_flag, c.fault);
+            a.next_kv_len[r] = c.kv;
+            a.next_pages_used[r] = c.need;
+        }
+        for (int j = threadIdx.x; j < a.max_pages; j += kPageThreads) {
+            int id = -1;
+            if (j < c.have) {
+                id = a.page_table[(size_t)c.par * a.max_pages + j];
+                if (id < 0 || id >= a.num_pages) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
+            } else if (j < c.need) {
+                id = (int)(base + (j - c.have));
+            }
+            a.next_table[(size_t)r * a.max_pages + j] = id;
+        }
+        if (r == a.R - 1) {
+            // pages handed out: the end of the last child that fits (the
+            // children after one that does not fit get none either)
+            __shared__ long long s_end;
+            if (threadIdx.x == 0) s_end = free0;
+            __syncthreads();
+            long long run = free0;
+            for (int i0 = 0; i0 < a.R; i0 += kPageThreads) {
+                const int i = i0 + (int)threadIdx.x;
+                int add = 0;
+                if (i < a.R) {
+                    const Child k = child_of(a, first_of, i);
+                    add = k.need - k.have;
+                }
+                long long incl = add;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const long long v = __shfl_up_sync(0xffffffffu, incl, off);
+                    if ((int)(threadIdx.x & 31) >= off) incl += v;
+                }
+                if ((threadIdx.x & 31) == 31) part[threadIdx.x >> 5] = incl;
+                __syncthreads();
+                for (int w = 0; w < (int)(threadIdx.x >> 5); ++w) incl += part[w];
+                const long long end = run + incl;
+                if (add > 0 && end <= a.num_pages) atomicMax(&s_end, end);
+                for (int w = 0; w < kPageThreads / 32; ++w) run += part[w];
+                __syncthreads();
+            }
+            if (threadIdx.x == 0) *a.next_free_out = (int)s_end;
+        }
+    }
+    // the part-filled page: the rows before kv_len go to the child's own page
+    const int tail = c.par >= 0 ? c.kv % a.P : 0;
+    if (tail == 0 || c.first) return;
+    const int src = a.page_table[(size_t)c.par * a.max_pages + c.have];
+    if (src < 0 || src >= a.num_pages) {
+        if (blockIdx.y == 0 && threadIdx.x == 0) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
+        return;
+    }
+    const int vecs = (int)((size_t)tail * a.row_bytes / 16);
+    for (int p = blockIdx.y; p < a.n_pools; p += gridDim.y) {
+        char* pool = static_cast<char*>(pools.p[p]);
+        const uint4* from = reinterpret_cast<const uint4*>(pool + (size_t)src * a.page_bytes);
+        uint4* to = reinterpret_cast<uint4*>(pool + (size_t)base * a.page_bytes);
+        for (int i = threadIdx.x; i < vecs; i += kPageThreads) to[i] = from[i];
+    }
+}
+
+struct CompactArgs {
+    int B, num_pages, max_pages, n_pools;
+    size_t page_bytes;
+    const int32_t* pages_used;
+    const int32_t* page_table;
+    int32_t* next_table;
+    int32_t* next_free_out;
+    uint32_t* live;  // bitmap of the pages in use
+    int32_t* moves;  // number of pages that move, then their old and new places
+    int32_t* err_flag;
+};
+
+// One CTA per request: marks its pages.
+__global__ void __launch_bounds__(kPageThreads) mark_kernel(const __grid_constant__ CompactArgs a) {
+    const int b = blockIdx.x;
+    int used = a.pages_used[b];
+    if (used < 0 || used > a.max_pages) {
+        if (threadIdx.x == 0) raise_flag(a.err_flag, ISD_FLAG_CAPACITY);
+        used = min(max(used, 0), a.max_pages);
+    }
+    for (int j = threadIdx.x; j < used; j += kPageThreads) {
+        const int id = a.page_table[(size_t)b * a.max_pages + j];
+        if (id < 0 || id >= a.num_pages) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
+        else atomicOr(&a.live[id >> 5], 1u << (id & 31));
+    }
+}
+
+// Exclusive scan over the CTA; returns the total.
+ISD_DEVINL int block_scan(int v, int& before, int* part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += u;
+    }
+    if (lane == 31) part[warp] = incl;
+    __syncthreads();
+    int base = 0, total = 0;
+    for (int w = 0; w < kPageThreads / 32; ++w) {
+        if (w < warp) base += part[w];
+        total += part[w];
+    }
+    __syncthreads();
+    before = base + incl - v;
+    return total;
+}
+
+// One CTA: L pages are in use; the k-th used page at or past L moves to the
+// k-th free place before L.
+__global__ void __launch_bounds__(kPageThreads) plan_kernel(const __grid_constant__ CompactArgs a) {
+    __shared__ int part[kPageThreads / 32];
+    const int words = (a.num_pages + 31) / 32;
+    int count = 0;
+    for (int w0 = 0; w0 < words; w0 += kPageThreads) {
+        const int w = w0 + (int)threadIdx.x;
+        int before;
+        count += block_scan(w < words ? __popc(a.live[w]) : 0, before, part);
+    }
+    int holes = 0, movers = 0;
+    int32_t* src = a.moves + 1;
+    int32_t* dst = src + a.num_pages;
+    for (int w0 = 0; w0 < words; w0 += kPageThreads) {
+        const int w = w0 + (int)threadIdx.x;
+        const uint32_t bits = w < words ? a.live[w] : 0;
+        // pages of this word that lie before / from L on
+        const int below = min(max(count - 32 * w, 0), 32);
+        const uint32_t low = below == 32 ? 0xffffffffu : ((1u << below) - 1);
+        uint32_t h = w < words ? ~bits & low : 0, m = bits & ~low;
+        int hb, mb;
+        const int ht = block_scan(__popc(h), hb, part), mt = block_scan(__popc(m), mb, part);
+        for (int k = holes + hb; h; h &= h - 1) dst[k++] = 32 * w + __ffs(h) - 1;
+        for (int k = movers + mb; m; m &= m - 1) src[k++] = 32 * w + __ffs(m) - 1;
+        holes += ht;
+        movers += mt;
+    }
+    if (threadIdx.x == 0) {
+        a.moves[0] = movers;
+        *a.next_free_out = count;
+    }
+}
+
+// New place of every page that moves, by its old one.
+__global__ void __launch_bounds__(kPageThreads) place_kernel(const __grid_constant__ CompactArgs a) {
+    const int n = a.moves[0];
+    const int32_t* src = a.moves + 1;
+    const int32_t* dst = src + a.num_pages;
+    int32_t* to = a.moves + 1 + 2 * (size_t)a.num_pages;
+    for (int i = blockIdx.x * kPageThreads + threadIdx.x; i < n; i += gridDim.x * kPageThreads) to[src[i]] = dst[i];
+}
+
+// The moves of all pools, one warp per piece of a page, and (with `tables`)
+// the page tables.
+constexpr int kMovePiece = 4096;
+__global__ void __launch_bounds__(kPageThreads) move_kernel(const __grid_constant__ CompactArgs a,
+                                                            const __grid_constant__ PoolList pools, int tables) {
+    const int n = a.moves[0];
+    const int32_t* src = a.moves + 1;
+    const int32_t* dst = src + a.num_pages;
+    const int32_t* to = a.moves + 1 + 2 * (size_t)a.num_pages;
+    const int live = *a.next_free_out;
+    if (tables) {
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+            const int used = min(max(a.pages_used[b], 0), a.max_pages);
+            for (int j = threadIdx.x; j < a.max_pages; j += kPageThreads) {
+                int id = -1;
+                if (j < used) {
+                    id = a.page_table[(size_t)b * a.max_pages + j];
+                    if (id >= live && id < a.num_pages) id = to[id];
+                }
+                a.next_table[(size_t)b * a.max_pages + j] = id;
+            }
+        }
+    }
+    const int lane = threadIdx.x & 31;
+    const int pieces = (int)((a.page_bytes + kMovePiece - 1) / kMovePiece);
+    const long long items = (long long)n * pieces * a.n_pools;
+    const long long warps = (long long)gridDim.x * (kPageThreads / 32);
+    for (long long it = (long long)blockIdx.x * (kPageThreads / 32) + (threadIdx.x >> 5); it < items; it += warps) {
+        const int piece = (int)(it % pieces);
+        const long long q = it / pieces;
+        const int k = (int)(q % n), p = (int)(q / n);
+        char* pool = static_cast<char*>(pools.p[p]);
+        const size_t off = (size_t)piece * kMovePiece;
+        const uint4* from = reinterpret_cast<const uint4*>(pool + (size_t)src[k] * a.page_bytes + off);
+        uint4* dest = reinterpret_cast<uint4*>(pool + (size_t)dst[k] * a.page_bytes + off);
+        const size_t left = a.page_bytes - off;
+        const int vecs = (int)((left < kMovePiece ? left : kMovePiece) / 16);
+        for (int i = lane; i < vecs; i += 32) dest[i] = from[i];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_fork(const isd_dims* d, int R, const int32_t* parent, const int32_t* reserve,
+                        const int32_t* kv_len, const int32_t* pages_used, const int32_t* page_table,
+                        const int32_t* next_free, int n_pools, uint16_t* const* pools,
+                        int32_t* next_kv_len, int32_t* next_pages_used, int32_t* next_table,
+                        int32_t* next_free_out, int32_t* err_flag, cudaStream_t st) {
+    ForkArgs a;
+    a.B = d->B;
+    a.R = R;
+    a.P = d->page_size;
+    a.num_pages = d->num_pages;
+    a.max_pages = d->max_pages_per_req;
+    a.n_pools = 0;
+    a.row_bytes = (size_t)d->Hkv * d->D * 2;
+    a.page_bytes = a.row_bytes * d->page_size;
+    a.parent = parent;
+    a.reserve = reserve;
+    a.kv_len = kv_len;
+    a.pages_used = pages_used;
+    a.page_table = page_table;
+    a.next_free = next_free;
+    a.next_kv_len = next_kv_len;
+    a.next_pages_used = next_pages_used;
+    a.next_table = next_table;
+    a.next_free_out = next_free_out;
+    a.err_flag = err_flag;
+    for (int p0 = 0; p0 == 0 || p0 < n_pools; p0 += kPoolsPerLaunch) {
+        PoolList list;
+        a.n_pools = n_pools - p0 < kPoolsPerLaunch ? n_pools - p0 : kPoolsPerLaunch;
+        for (int i = 0; i < a.n_pools; ++i) list.p[i] = pools[p0 + i];
+        const cudaError_t e = launch_kernel(false, fork_kernel, dim3(R, a.n_pools > 0 ? a.n_pools : 1),
+                                            dim3(kPageThreads), (size_t)d->B * 4, st, a, list);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_compact(const isd_dims* d, const int32_t* pages_used, const int32_t* page_table,
+                           int n_pools, uint16_t* const* pools, int32_t* next_table,
+                           int32_t* next_free_out, void* ws, int32_t* err_flag, cudaStream_t st) {
+    CompactArgs a;
+    a.B = d->B;
+    a.num_pages = d->num_pages;
+    a.max_pages = d->max_pages_per_req;
+    a.page_bytes = (size_t)d->page_size * d->Hkv * d->D * 2;
+    a.pages_used = pages_used;
+    a.page_table = page_table;
+    a.next_table = next_table;
+    a.next_free_out = next_free_out;
+    a.live = static_cast<uint32_t*>(ws);
+    a.moves = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + align_up((size_t)(d->num_pages + 31) / 32 * 4, 256));
+    a.err_flag = err_flag;
+    cudaError_t e = cudaMemsetAsync(a.live, 0, (size_t)(d->num_pages + 31) / 32 * 4, st);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(false, mark_kernel, dim3(d->B), dim3(kPageThreads), 0, st, a);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(false, plan_kernel, dim3(1), dim3(kPageThreads), 0, st, a);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(false, place_kernel, dim3(persistent_grid()), dim3(kPageThreads), 0, st, a);
+    if (e != cudaSuccess) return e;
+    for (int p0 = 0; p0 == 0 || p0 < n_pools; p0 += kPoolsPerLaunch) {
+        PoolList list;
+        a.n_pools = n_pools - p0 < kPoolsPerLaunch ? n_pools - p0 : kPoolsPerLaunch;
+        for (int i = 0; i < a.n_pools; ++i) list.p[i] = pools[p0 + i];
+        e = launch_kernel(false, move_kernel, dim3(8 * persistent_grid()), dim3(kPageThreads), 0, st, a, list, p0 == 0 ? 1 : 0);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace isd

@@ -69,6 +69,27 @@ struct Plan {
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Pools (a layer's K or V cache each) that one launch of a page kernel takes:
+// their pointers travel as kernel arguments.
+constexpr int kPoolsPerLaunch = 128;
+struct PoolList {
+    void* p[kPoolsPerLaunch];
+};
+
+// Workspace of isd_compact_pages: a bitmap of the pages in use, then the
+// number of moves, their old and new places, and the new place by old page.
+inline size_t pages_ws_bytes(const isd_dims* d) {
+    return align_up((size_t)(d->num_pages + 31) / 32 * 4, 256) +
+           align_up((1 + 3 * (size_t)d->num_pages) * 4, 256);
+}
+
+// Workspace of isd_chunk_attention.
+inline size_t chunk_ws_bytes(const isd_dims* d, int T) {
+    (void)d;
+    (void)T;
+    return 256;
+}
+
 // SMs of the current device, capped at kMaxSMs (cached per device).  The one
 // place the persistent kernels take their grid size from.
 int persistent_grid();

@@ -32,13 +32,17 @@ FLAG_TOKEN_OOB = 2
 FLAG_NCLEAN_RANGE = 4
 FLAG_CAPACITY = 8
 FLAG_WAIT_TIMEOUT = 16
+FLAG_CHUNK_RANGE = 32
+FLAG_PARENT_OOB = 64
 PROPOSE_ARGMAX = 0
 PROPOSE_SAMPLE = 1
 
 EXPORTED = ("isd_workspace_bytes", "isd_status_string", "isd_last_error", "isd_attention",
             "isd_lm_head", "isd_row_stats", "isd_accept", "isd_step", "isd_prepare_block",
             "isd_loop", "isd_attention_noalloc", "isd_sdar_step", "isd_sdar_unmask",
-            "isd_sdar_loop", "isd_layers_workspace_bytes", "isd_layers", "isd_embed_block")
+            "isd_sdar_loop", "isd_layers_workspace_bytes", "isd_layers", "isd_embed_block",
+            "isd_chunk_workspace_bytes", "isd_chunk_attention", "isd_fork_requests",
+            "isd_pages_workspace_bytes", "isd_compact_pages")
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # ISD_NOALLOC_SCRATCH_BYTES in include/isd.h
 
 
@@ -140,6 +144,16 @@ _lib.isd_layers.argtypes = [_dims_p, _i32, _i32, _f32, ctypes.POINTER(Layer), _v
 _lib.isd_layers.restype = _i32
 _lib.isd_embed_block.argtypes = [_dims_p] + [_vp] * 6
 _lib.isd_embed_block.restype = _i32
+_lib.isd_chunk_workspace_bytes.argtypes = [_dims_p, _i32]
+_lib.isd_chunk_workspace_bytes.restype = _sz
+_lib.isd_chunk_attention.argtypes = [_dims_p, _i32] + [_vp] * 10 + [_sz, _vp, _vp]
+_lib.isd_chunk_attention.restype = _i32
+_lib.isd_fork_requests.argtypes = [_dims_p, _i32] + [_vp] * 6 + [_i32] + [_vp] * 7
+_lib.isd_fork_requests.restype = _i32
+_lib.isd_pages_workspace_bytes.argtypes = [_dims_p]
+_lib.isd_pages_workspace_bytes.restype = _sz
+_lib.isd_compact_pages.argtypes = [_dims_p] + [_vp] * 2 + [_i32] + [_vp] * 4 + [_sz, _vp, _vp]
+_lib.isd_compact_pages.restype = _i32
 
 
 class IsdError(RuntimeError):
@@ -528,3 +542,169 @@ def embed_block(d: Dims, E, n_clean, clean_tok, x, err_flag=None, stream=None):
         ctypes.byref(d), _ptr(E, _BF16, (d.V + 1) * H, "E"), _ptr(n_clean, torch.int32, d.B, "n_clean"),
         _ptr(clean_tok, torch.int32, d.B * d.N, "clean_tok"), _ptr(x, _BF16, d.M * H, "x"),
         _ptr(err_flag, torch.int32, 1, "err_flag"), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Prompts and pages
+# ---------------------------------------------------------------------------
+def _on_device(tensors, stream):
+    """The tensors' one device, made current for the call, and the stream to
+    use there: a CUDA launch takes both from the calling thread."""
+    dev = None
+    for name, t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+    return torch.cuda.device(dev), \
+        torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+
+
+def chunk_workspace_bytes(d: Dims, T: int) -> int:
+    return int(_lib.isd_chunk_workspace_bytes(ctypes.byref(d), int(T)))
+
+
+def alloc_chunk_workspace(d: Dims, T: int, device="cuda") -> torch.Tensor:
+    """Workspace of chunk_attention for at most T rows."""
+    n = chunk_workspace_bytes(d, T)
+    if n == 0:
+        raise IsdError(ISD_ERR_INVALID_ARG)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+class ChunkCall:
+    """isd_chunk_attention with its arguments checked and marshalled once.
+
+    For a program whose buffers stay in place (StepCall's counterpart): the
+    constructor takes the arguments of ``chunk_attention`` and validates them;
+    calling the object passes the cached pointers to the library.  With
+    stream=None each call goes to the stream that is current then.  The tensors
+    must stay alive and in place while the object is used."""
+
+    def __init__(self, d: Dims, q, k_new, v_new, k_pool, v_pool, page_table, kv_len, q_start, out,
+                 ws, err_flag=None, stream=None):
+        if d.Hq < 1 or d.Hkv < 1 or d.D < 1:
+            raise IsdError(ISD_ERR_INVALID_ARG)
+        T = q.numel() // (d.Hq * d.D)
+        kvrow = d.page_size * d.Hkv * d.D
+        named = [
+            ("q", q, _BF16, T * d.Hq * d.D), ("k_new", k_new, _BF16, T * d.Hkv * d.D),
+            ("v_new", v_new, _BF16, T * d.Hkv * d.D), ("k_pool", k_pool, _BF16, d.num_pages * kvrow),
+            ("v_pool", v_pool, _BF16, d.num_pages * kvrow),
+            ("page_table", page_table, torch.int32, d.B * d.max_pages_per_req),
+            ("kv_len", kv_len, torch.int32, d.B), ("q_start", q_start, torch.int32, d.B + 1),
+            ("out", out, _BF16, T * d.Hq * d.D), ("ws", ws, torch.uint8, None)]
+        ptrs = [_ptr(t, dt, n, name) for name, t, dt, n in named]
+        flag = _ptr(err_flag, torch.int32, 1, "err_flag")
+        tensors = [(name, t) for name, t, _, _ in named] + [("err_flag", err_flag)]
+        _on_device(tensors, stream)
+        self._keep = (d, tensors)  # the cached arguments point at them
+        self._device = q.device
+        self._stream = None if stream is None else _stream(stream)
+        self._args = (ctypes.byref(d), T, *ptrs, ws.numel(), flag)
+
+    def __call__(self):
+        st = self._stream
+        if st is None:
+            st = torch.cuda.current_stream(self._device).cuda_stream
+        if torch.cuda.current_device() == self._device.index:
+            _check(_lib.isd_chunk_attention(*self._args, st))
+        else:
+            with torch.cuda.device(self._device):
+                _check(_lib.isd_chunk_attention(*self._args, st))
+
+
+def chunk_attention(d: Dims, q, k_new, v_new, k_pool, v_pool, page_table, kv_len, q_start, out, ws,
+                    err_flag=None, stream=None):
+    """isd_chunk_attention: K/V append and causal attention of q_start[b+1] -
+    q_start[b] new tokens per request over the paged cache.  q [T, Hq, D],
+    k_new, v_new [T, Hkv, D], out [T, Hq*D]; ws: alloc_chunk_workspace(d, T)."""
+    ChunkCall(d, q, k_new, v_new, k_pool, v_pool, page_table, kv_len, q_start, out, ws, err_flag,
+              stream)()
+
+
+class PoolArray:
+    """Checked pool pointers of every layer (k_pool and v_pool of each)."""
+
+    def __init__(self, d: Dims, pools):
+        pools = list(pools)
+        kvrow = d.page_size * d.Hkv * d.D
+        self.ptrs = (_vp * max(len(pools), 1))()
+        self.count = len(pools)
+        self.numel = d.num_pages * kvrow
+        for i, t in enumerate(pools):
+            self.ptrs[i] = _ptr(t, _BF16, self.numel, f"pool {i}")
+            if t.device != pools[0].device:
+                raise ValueError(f"pool {i} is on {t.device}, pool 0 on {pools[0].device}")
+        self.tensors = pools  # keeps them alive
+
+
+def pool_array(d: Dims, pools) -> PoolArray:
+    """The pools of fork_requests and compact_pages, checked once: an iterable
+    of bf16 [num_pages, page_size, Hkv, D] tensors."""
+    return PoolArray(d, pools)
+
+
+def _pools(d: Dims, pools) -> PoolArray:
+    if not isinstance(pools, PoolArray):
+        return PoolArray(d, pools)
+    if pools.numel != d.num_pages * d.page_size * d.Hkv * d.D:
+        raise ValueError("the pool array was made for other dims")
+    return pools
+
+
+def fork_requests(d: Dims, parent, kv_len, pages_used, page_table, next_free_page, pools,
+                  next_kv_len, next_pages_used, next_page_table, next_free_out, reserve=None,
+                  err_flag=None, stream=None):
+    """isd_fork_requests: the batch whose slot r continues request parent[r]
+    (-1: empty), with room for reserve[r] more tokens.  pools: every layer's
+    k_pool and v_pool (an iterable of tensors, or a pool_array)."""
+    R, cols = parent.numel(), d.max_pages_per_req
+    pa = _pools(d, pools)
+    i32 = torch.int32
+    named = [("parent", parent, R), ("reserve", reserve, R), ("kv_len", kv_len, d.B),
+             ("pages_used", pages_used, d.B), ("page_table", page_table, d.B * cols),
+             ("next_free_page", next_free_page, 1)]
+    outs = [("next_kv_len", next_kv_len, R), ("next_pages_used", next_pages_used, R),
+            ("next_page_table", next_page_table, R * cols), ("next_free_out", next_free_out, 1)]
+    p_in = [_ptr(t, i32, n, name) for name, t, n in named]
+    p_out = [_ptr(t, i32, n, name) for name, t, n in outs]
+    flag = _ptr(err_flag, i32, 1, "err_flag")
+    guard, st = _on_device([(name, t) for name, t, _ in named + outs] + [("err_flag", err_flag)] +
+                           [("pools", t) for t in pa.tensors[:1]], stream)
+    with guard:
+        _check(_lib.isd_fork_requests(ctypes.byref(d), R, *p_in, pa.count, pa.ptrs, *p_out, flag,
+                                      st))
+
+
+def pages_workspace_bytes(d: Dims) -> int:
+    return int(_lib.isd_pages_workspace_bytes(ctypes.byref(d)))
+
+
+def alloc_pages_workspace(d: Dims, device="cuda") -> torch.Tensor:
+    """Workspace of compact_pages."""
+    n = pages_workspace_bytes(d)
+    if n == 0:
+        raise IsdError(ISD_ERR_INVALID_ARG)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def compact_pages(d: Dims, page_table, pages_used, pools, next_page_table, next_free_out, ws,
+                  err_flag=None, stream=None):
+    """isd_compact_pages: the pages in use become pages 0 .. L-1 of every pool
+    (next_free_out = L); next_page_table is the table after the move."""
+    pa = _pools(d, pools)
+    i32, n = torch.int32, d.B * d.max_pages_per_req
+    named = [("pages_used", pages_used, i32, d.B), ("page_table", page_table, i32, n)]
+    outs = [("next_page_table", next_page_table, i32, n), ("next_free_out", next_free_out, i32, 1),
+            ("ws", ws, torch.uint8, None)]
+    p_in = [_ptr(t, dt, k, name) for name, t, dt, k in named]
+    p_out = [_ptr(t, dt, k, name) for name, t, dt, k in outs]
+    flag = _ptr(err_flag, i32, 1, "err_flag")
+    guard, st = _on_device([(name, t) for name, t, _, _ in named + outs] +
+                           [("err_flag", err_flag)] + [("pools", t) for t in pa.tensors[:1]], stream)
+    with guard:
+        _check(_lib.isd_compact_pages(ctypes.byref(d), *p_in, pa.count, pa.ptrs, *p_out,
+                                      ws.numel(), flag, st))
