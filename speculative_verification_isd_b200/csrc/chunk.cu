@@ -1,149 +1,1014 @@
 // Attention of a chunk of new tokens per request over the paged cache: the
 // prompt's (and plain decoding's) counterpart of the block attention.  Row i
 // of request b is the token at position kv_len[b] + i; its K/V row goes to
-// its page and it attends to every key at a position <= its own.
+// its page and it attends to every key at a position <= its own:
+//
+//   out[i, h] = sum_j 2^(x_ij - m_i) v_j / sum_j 2^(x_ij - m_i),
+//   x_ij = sm_scale log2(e) q[i, h] . k_j,   j <= kv_len[b] + i.
+//
+// One persistent kernel, one CTA per SM, then a small one that joins the
+// pieces of work items cut between CTAs:
+//
+//  * rows are packed: a tile is up to 128 rows (token, head of the KV group),
+//    an item is up to two tiles of consecutive tokens of one (request, KV
+//    head), so a key tile read once serves 256 rows of a prompt, and every
+//    head of a group when decoding;
+//  * the items' 128-key tiles, flattened, are cut into one equal range per CTA
+//    (the lengths are on the device, so every CTA works the cut out itself);
+//  * cached keys come from their pages by TMA, new keys from k_new / v_new
+//    themselves, so nothing waits for the append, which a spare warp does on
+//    the side;
+//  * S = Q.K^T and O += P.V run on the tensor cores with S, P and O in TMEM
+//    (P overwrites S as bf16); a softmax thread owns one row, its maximum and
+//    sum live in registers, and O is rescaled only when a maximum grows by
+//    more than 2^8;
+//  * a prompt item keeps two tiles in flight (one warpgroup each), so that one
+//    tile's softmax runs under the other's products; an item of at most 128 rows
+//    (decoding) double-buffers S instead;
+//  * every wait is bounded (about 2 s): on time-out the CTA raises
+//    ISD_FLAG_WAIT_TIMEOUT, all roles leave their loops, copies and MMAs in
+//    flight are drained and TMEM is released.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
 #include "launch.h"
 #include "plan.h"
+#include "sm100.cuh"
+#include "tmap.h"
 
 namespace isd {
 
+void set_error_detail(const char* msg);
+
 namespace {
 
+constexpr int kKeys = 128;              // keys per tile
+constexpr int kTileRows = 128;          // rows per tile
+constexpr int kHalfBytes = kKeys * 128; // 64 dimensions of a K, V or Q tile
+constexpr uint64_t kWaitNs = 2000000000ull;
+// New tokens that are put into the free rows of the last cached tile instead
+// of a tile of their own.
+constexpr int kMergeTokens = 16;
+// Cost of a key tile and of an item's start and end on the partition axis: an
+// item of two row tiles, and one of one.
+constexpr int kCost2 = 3, kEnds2 = 4, kCost1 = 2, kEnds1 = 2;
+constexpr int kChunkThreads = 384;
+constexpr int kLaunchRegs = 168, kRegsLow = 88, kRegsHigh = 208;
+static_assert(kRegsLow * 128 + kRegsHigh * 256 <= kLaunchRegs * kChunkThreads, "register split exceeds the launch");
+
+// A cut item, for the joining kernel (written by the CTA with its first keys).
+struct ChunkCut {
+    int parts;  // CTAs that hold a part, from the writing one on; 0: nothing cut
+    int g, i0, i1, start;
+    int pad[3];
+};
+
 struct ChunkArgs {
-    int B, T, Hq, Hkv, grp, P, num_pages, max_pages;
+    int B, T, Hq, Hkv, grp, tpq, P, box, num_pages, max_pages;
+    int cost_max;   // the dearest key tile that this T allows
+    int part_rows;  // rows of a partial result
     float scale_log2;
     const int32_t* page_table;
     const int32_t* kv_len;
     const int32_t* q_start;
-    const __nv_bfloat16* q;
     const __nv_bfloat16* k_new;
     const __nv_bfloat16* v_new;
     __nv_bfloat16* k_pool;
     __nv_bfloat16* v_pool;
     __nv_bfloat16* out;
+    float* part;    // [grid][2] partials: maxima, sums [part_rows], O [D][part_rows]
+    ChunkCut* cuts;  // [grid]
     int32_t* err_flag;
 };
 
-constexpr int kAppendTokens = 8;  // tokens (warps) per append CTA
-
 // New tokens of request b if its page list can hold them, else 0 (negative
 // or over-capacity length).  q_start is known to ascend within [0, T].
-ISD_DEVINL int chunk_tokens(const ChunkArgs& a, int b, int kv, int n) {
+ISD_DEVINL int chunk_tokens(const ChunkArgs& a, int kv, int n) {
     if (kv < 0) return 0;
     const long long t = (long long)kv + n;
     return (t + a.P - 1) / a.P > a.max_pages ? 0 : n;
 }
 
-// Whether q_start ascends within [0, T] (every thread of the CTA gets the answer).
-ISD_DEVINL bool chunk_starts_ok(const ChunkArgs& a) {
-    bool bad = false;
-    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-        const int s = a.q_start[b], e = a.q_start[b + 1];
-        bad |= s < 0 || e < s || e > a.T;
-    }
-    return !__syncthreads_or(bad);
+// A request as the partition sees it.
+struct Request {
+    int n, kv, start;
+    int kvt;      // tiles with cached keys
+    bool merged;  // the new tokens lie in the last of them
+    int items;    // per KV head
+};
+
+ISD_DEVINL Request request_of(const ChunkArgs& a, int b) {
+    Request r;
+    r.start = a.q_start[b];
+    r.kv = a.kv_len[b];
+    r.n = chunk_tokens(a, r.kv, a.q_start[b + 1] - r.start);
+    r.kvt = (max(r.kv, 0) + kKeys - 1) / kKeys;
+    r.merged = r.n <= kMergeTokens && r.n <= r.kvt * kKeys - r.kv;
+    r.items = (r.n + 2 * a.tpq - 1) / (2 * a.tpq);
+    return r;
 }
 
-// The request of token t (a warp asks together): the last b with
-// q_start[b] <= t, or -1 for a row of no request.
-ISD_DEVINL int chunk_request(const ChunkArgs& a, int t) {
-    const int lane = threadIdx.x & 31;
-    int count = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int b = b0 + lane;
-        count += __popc(__ballot_sync(0xffffffffu, b < a.B && a.q_start[b] <= t));
-    }
-    const int b = count - 1;
-    return b >= 0 && t < a.q_start[b + 1] ? b : -1;
+ISD_DEVINL int item_end(const ChunkArgs& a, const Request& r, int q) { return min(r.n, (q + 1) * 2 * a.tpq); }
+ISD_DEVINL bool item_two(const ChunkArgs& a, const Request& r, int q) {
+    return item_end(a, r, q) - q * 2 * a.tpq > a.tpq;
+}
+ISD_DEVINL int item_tiles(const ChunkArgs& a, const Request& r, int q) {
+    return r.kvt + (r.merged ? 0 : (item_end(a, r, q) + kKeys - 1) / kKeys);
+}
+ISD_DEVINL int item_cost(const ChunkArgs& a, const Request& r, int q) {
+    const int nt = item_tiles(a, r, q);
+    return item_two(a, r, q) ? kCost2 * nt + kEnds2 : kCost1 * nt + kEnds1;
+}
+ISD_DEVINL long long head_cost(const ChunkArgs& a, const Request& r) {
+    long long c = 0;
+    for (int q = 0; q < r.items; ++q) c += item_cost(a, r, q);
+    return c;
 }
 
-// One warp per token: its K and V rows go into their page, 16 bytes per lane
-// and step; a request that cannot be served gets zero output rows.
-template <int D>
-__global__ void __launch_bounds__(32 * kAppendTokens) chunk_append_kernel(const __grid_constant__ ChunkArgs a) {
-    const bool ok = chunk_starts_ok(a);
-    if (!ok) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) raise_flag(a.err_flag, ISD_FLAG_CHUNK_RANGE);
-        return;
-    }
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kAppendTokens + (threadIdx.x >> 5);
-    if (t >= a.T) return;
-    const int b = chunk_request(a, t);
-    if (b < 0) return;
-    const int start = a.q_start[b], kv = a.kv_len[b];
-    if (chunk_tokens(a, b, kv, a.q_start[b + 1] - start) == 0) {
-        if (lane == 0) raise_flag(a.err_flag, ISD_FLAG_CAPACITY);
-        uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)t * a.Hq * D);
-        for (int i = lane; i < a.Hq * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
-        return;
-    }
-    const int pos = kv + (t - start);
-    const int page = a.page_table[(size_t)b * a.max_pages + pos / a.P];
-    if (page < 0 || page >= a.num_pages) {
-        if (lane == 0) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
-        return;
-    }
-    const size_t dst = ((size_t)page * a.P + pos % a.P) * a.Hkv * D, src = (size_t)t * a.Hkv * D;
-    for (int i = lane; i < a.Hkv * D / 8; i += 32) {
-        reinterpret_cast<uint4*>(a.k_pool + dst)[i] = reinterpret_cast<const uint4*>(a.k_new + src)[i];
-        reinterpret_cast<uint4*>(a.v_pool + dst)[i] = reinterpret_cast<const uint4*>(a.v_new + src)[i];
-    }
-}
+// This CTA's share of one item: key tiles [t0, t1).
+struct Piece {
+    int b, g, q;
+    long long us;  // the item's start on the partition axis
+    Request r;
+    bool two;
+    int nt, cost, t0, t1;
+    int i0, i1;    // its tokens
+};
 
-// One warp per (token, query head); each lane owns D / 32 dimensions and the
-// warp walks the visible keys with a running maximum and sum.
-template <int D>
-__global__ void __launch_bounds__(128) chunk_attention_kernel(const __grid_constant__ ChunkArgs a) {
-    constexpr int E = D / 32;
-    if (!chunk_starts_ok(a)) return;
-    const int lane = threadIdx.x & 31;
-    const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (id >= (long long)a.T * a.Hq) return;
-    const int t = (int)(id / a.Hq), h = (int)(id % a.Hq), g = h / a.grp;
-    const int b = chunk_request(a, t);
-    if (b < 0) return;
-    const int start = a.q_start[b], kv = a.kv_len[b];
-    if (chunk_tokens(a, b, kv, a.q_start[b + 1] - start) == 0) return;
-    float qv[E], o[E];
-    for (int e = 0; e < E; ++e) {
-        qv[e] = __bfloat162float(a.q[((size_t)t * a.Hq + h) * D + lane * E + e]);
-        o[e] = 0.f;
+// Walks the CTA's range [my0, my1); the order is request, KV head, item.
+struct Walker {
+    const ChunkArgs& a;
+    long long my0, my1;
+    Piece p;
+
+    ISD_DEVINL void fill() {
+        p.two = item_two(a, p.r, p.q);
+        p.nt = item_tiles(a, p.r, p.q);
+        p.cost = item_cost(a, p.r, p.q);
+        p.i0 = p.q * 2 * a.tpq;
+        p.i1 = item_end(a, p.r, p.q);
+        const int w = p.two ? kCost2 : kCost1;
+        const long long lo = my0 - p.us, hi = my1 - p.us;
+        p.t0 = lo <= 0 ? 0 : (int)((lo + w - 1) / w);
+        p.t1 = (int)min((long long)p.nt, (hi + w - 1) / w);
     }
-    float m = -INFINITY, l = 0.f;
-    const int last = kv + (t - start);
-    for (int key = 0; key <= last; ++key) {
-        const int page = a.page_table[(size_t)b * a.max_pages + key / a.P];
-        const bool bad = page < 0 || page >= a.num_pages;
-        if (bad && lane == 0) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
-        const size_t row = bad ? 0 : (((size_t)page * a.P + key % a.P) * a.Hkv + g) * D + lane * E;
-        float s = 0.f, v[E];
-        for (int e = 0; e < E; ++e) {
-            s += bad ? 0.f : qv[e] * __bfloat162float(a.k_pool[row + e]);
-            v[e] = bad ? 0.f : __bfloat162float(a.v_pool[row + e]);
+    ISD_DEVINL void step() {
+        p.us += p.cost;
+        if (++p.q < p.r.items) return;
+        p.q = 0;
+        if (++p.g < a.Hkv) return;
+        p.g = 0;
+        do {
+            if (++p.b >= a.B) return;
+            p.r = request_of(a, p.b);
+        } while (p.r.items == 0);
+    }
+    // to the first piece with a tile, starting from the item the walker is at
+    ISD_DEVINL bool settle() {
+        while (p.b < a.B && p.us < my1) {
+            fill();
+            if (p.t0 < p.t1) return true;
+            step();
         }
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= a.scale_log2;
-        const float mn = fmaxf(m, s), mu = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(m - mu), p = exp2f(s - mu);
-        l = l * f + p;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * v[e];
-        m = mn;
+        return false;
     }
-    for (int e = 0; e < E; ++e)
-        a.out[((size_t)t * a.Hq + h) * D + lane * E + e] = __float2bfloat16_rn(o[e] / l);
+    ISD_DEVINL bool next() {
+        step();
+        return settle();
+    }
+    // a piece that is not the whole item leaves a partial: slot 0 when the
+    // item began before this range, 1 when it goes on past it
+    ISD_DEVINL int slot() const { return p.t0 > 0 ? 0 : p.t1 < p.nt ? 1 : -1; }
+};
+
+template <int D>
+struct ChunkShape {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTile = kHalves * kHalfBytes;  // bytes of a Q, K or V tile
+    static constexpr int kStages = D == 128 ? 5 : 10;   // ring of K and V tiles
+    static constexpr size_t kSmem() { return 1024 + (size_t)(2 + kStages) * kTile + 2048; }
+};
+
+template <int D>
+struct ChunkShared {
+    static constexpr int S = ChunkShape<D>::kStages;
+    uint64_t full[S], empty[S], fix[S];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2];    // two-tile items: by tile
+    uint64_t s1_full[2], p1_full[2];  // one-tile items: by S buffer
+    uint64_t pv_done[2], o_free[2], drain;
+    long long my0, my1, us;
+    int b, g, q;
+    uint32_t tmem;
+    int abort_flag, never;
+    int epilogues;   // finished by softmax warps
+    int bad_piece;   // the piece whose `bad_from` holds, or -1
+    int bad_from[3][D];  // first new token with +inf, -inf, NaN in dimension d of V
+};
+
+ISD_DEVINL float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+ISD_DEVINL void tmem_st32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// D(tmem) (+)= A(tmem) * B(smem desc), kind::f16
+ISD_DEVINL void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+ISD_DEVINL uint64_t policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(p));
+    return p;
+}
+
+// Whether one of two packed bf16 is infinite or NaN.
+ISD_DEVINL bool odd_pair(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
+
+template <int D>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kn,
+             const __grid_constant__ CUtensorMap tm_vn, const __grid_constant__ ChunkArgs a) {
+    using namespace sm100;
+    using Shape = ChunkShape<D>;
+    constexpr int NH = Shape::kHalves, NST = Shape::kStages;
+    constexpr uint32_t kTmemCols = 512, kTmemO = 256;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* sQ = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~uintptr_t(1023));
+    unsigned char* ring = sQ + 2 * Shape::kTile;
+    ChunkShared<D>* sh = reinterpret_cast<ChunkShared<D>*>(ring + NST * Shape::kTile);
+    static_assert(sizeof(ChunkShared<D>) <= 2048, "control block");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_trigger();
+
+    // ---- set-up: barriers, TMEM, and this CTA's range of the work
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(&sh->full[s], 1);
+            mbar_init(&sh->empty[s], 1);
+            mbar_init(&sh->fix[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->q_full[i], 1);
+            mbar_init(&sh->q_empty[i], 1);
+            mbar_init(&sh->s_full[i], 1);
+            mbar_init(&sh->s1_full[i], 1);
+            mbar_init(&sh->p_full[i], 4);
+            mbar_init(&sh->p1_full[i], 4);
+            mbar_init(&sh->pv_done[i], 1);
+            mbar_init(&sh->o_free[i], 4);
+        }
+        mbar_init(&sh->drain, 1);
+        sh->abort_flag = sh->never = 0;
+        sh->epilogues = 0;
+        sh->bad_piece = -1;
+        sh->b = a.B;
+        fence_mbar_init();
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+        prefetch_tmap(&tm_kn);
+        prefetch_tmap(&tm_vn);
+        a.cuts[blockIdx.x].parts = 0;
+    }
+    if (warp == 8) {
+        tmem_alloc(&sh->tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    bool bad = false;
+    long long total = 0;
+    // costs of the requests, summed in order: the whole first, then again up to
+    // the request that holds this CTA's first position
+    {
+        long long* wsum = reinterpret_cast<long long*>(ring);  // 12 warp sums (the ring is not in use yet)
+        const long long none = -1;
+        long long my0 = none, my1 = none;
+        for (int pass = 0; pass < 2; ++pass) {
+            long long run = 0;
+            for (int b0 = 0; b0 < a.B; b0 += kChunkThreads) {
+                const int b = b0 + (int)threadIdx.x;
+                long long c = 0;
+                Request r = {};
+                if (b < a.B) {
+                    const int s = a.q_start[b], e = a.q_start[b + 1];
+                    if (s < 0 || e < s || e > a.T) bad = true;
+                    else {
+                        r = request_of(a, b);
+                        c = head_cost(a, r) * a.Hkv;
+                    }
+                }
+                long long incl = c;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const long long v = __shfl_up_sync(0xffffffffu, incl, off);
+                    if (lane >= off) incl += v;
+                }
+                __syncthreads();
+                if (lane == 31) wsum[warp] = incl;
+                __syncthreads();
+                long long before = run;
+                for (int w = 0; w < kChunkThreads / 32; ++w) {
+                    if (w < warp) before += wsum[w];
+                    run += wsum[w];
+                }
+                before += incl - c;
+                if (pass == 1 && my0 < my1 && before <= my0 && my0 < before + c) {
+                    long long rem = my0 - before;
+                    const long long hc = c / a.Hkv;
+                    const int g = (int)(rem / hc);
+                    rem -= g * hc;
+                    int q = 0;
+                    for (int w; (w = item_cost(a, r, q)) <= rem; ++q) rem -= w;
+                    sh->b = b;
+                    sh->g = g;
+                    sh->q = q;
+                    sh->us = my0 - rem;
+                }
+            }
+            if (pass == 0) {
+                total = run;
+                const long long most = total / a.cost_max;  // every CTA between an item's ends has a tile of it
+                const int G = (int)min((long long)gridDim.x, max(most, 1ll));
+                const bool mine = (int)blockIdx.x < G;
+                my0 = mine ? total * blockIdx.x / G : 0;
+                my1 = mine ? total * (blockIdx.x + 1) / G : 0;
+                if (threadIdx.x == 0) {
+                    sh->my0 = my0;
+                    sh->my1 = my1;
+                }
+            }
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    tc_fence_before();
+    bad = __syncthreads_or(bad);
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem;
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) raise_flag(a.err_flag, ISD_FLAG_CHUNK_RANGE);
+    volatile int* abort_flag = &sh->abort_flag;
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        raise_flag(a.err_flag, ISD_FLAG_WAIT_TIMEOUT);
+    };
+    Walker wk{a, sh->my0, sh->my1, {}};
+    wk.p.b = bad ? a.B : sh->b;
+    wk.p.g = sh->g;
+    wk.p.q = sh->q;
+    wk.p.us = sh->us;
+    if (wk.p.b < a.B) wk.p.r = request_of(a, wk.p.b);
+
+    if (warp >= 8) {
+        setmaxnreg_dec<kRegsLow>();
+        if (warp == 8) {
+            // ------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = idesc_bf16_f32(kTileRows, kKeys);
+                constexpr uint32_t idesc_o = idesc_bf16_f32(kTileRows, D) | (1u << 16);  // B = V: keys by rows
+                const uint64_t dq = smem_desc_sw128(smem_u32(sQ));
+                const uint64_t dk = smem_desc_sw128(smem_u32(ring));
+                // V as an operand with its dimensions contiguous: the two 64-d
+                // halves are kHalfBytes apart, 8-key groups 1024 bytes
+                const uint64_t dv = (dk & ~(0x3FFFull << 16)) | ((uint64_t)(kHalfBytes >> 4) << 16);
+                uint32_t rc = 0;             // ring position of the piece's first K tile
+                uint32_t fixes = 0;          // per stage: parity of the next fix
+                uint32_t q_use[2] = {0, 0}, n2 = 0, n1[2] = {0, 0}, pieces[2] = {0, 0};
+                uint32_t ones = 0;
+                bool ok = true;
+                auto wait = [&](uint64_t* bar, uint32_t par) {
+                    if (ok && !mbar_wait_bounded(bar, par & 1, abort_flag, kWaitNs)) {
+                        give_up();
+                        ok = false;
+                    }
+                    return ok;
+                };
+                auto take = [&](uint32_t pos, bool fixed) {  // the tile at ring position pos is there
+                    const uint32_t s = pos % NST;
+                    if (!wait(&sh->full[s], pos / NST)) return false;
+                    if (fixed) {
+                        if (!wait(&sh->fix[s], fixes >> s)) return false;
+                        fixes ^= 1u << s;
+                    }
+                    tc_fence_after();
+                    return true;
+                };
+                auto s_product = [&](int buf, int qs, uint32_t pos) {
+                    const uint32_t k_off = (pos % NST) * Shape::kTile, q_off = (uint32_t)qs * Shape::kTile;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t in = (uint32_t)((kk >> 2) * kHalfBytes + (kk & 3) * 32);
+                        mma_f16_ss(tmem + buf * kKeys, dq + ((q_off + in) >> 4), dk + ((k_off + in) >> 4), idesc_s,
+                                   kk != 0);
+                    }
+                };
+                auto pv_product = [&](int o, int buf, uint32_t pos, bool first) {
+                    const uint32_t v_off = (pos % NST) * Shape::kTile;
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        mma_f16_ts(tmem + kTmemO + o * D, tmem + buf * kKeys + kk * 8, dv + ((v_off + kk * 2048) >> 4),
+                                   idesc_o, !(first && kk == 0));
+                };
+                for (bool has = wk.settle(); ok && has; has = wk.next()) {
+                    const Piece& p = wk.p;
+                    const int nt = p.t1 - p.t0;
+                    // which tiles the fixing warp touches first
+                    auto k_fixed = [&](int k) { return p.r.merged && p.t0 + k == p.r.kvt - 1; };
+                    auto v_fixed = [&](int k) {
+                        const int t = p.t0 + k;
+                        if (t < p.r.kvt) return (t + 1) * kKeys > p.r.kv;
+                        return (t + 1 - p.r.kvt) * kKeys > p.i0 + 1;
+                    };
+                    auto k_pos = [&](int k) { return rc + 2 * k; };
+                    auto v_pos = [&](int k) { return rc + 2 * k + 1; };
+                    auto free_stage = [&](uint32_t pos) { mma_commit(&sh->empty[pos % NST]); };
+                    if (p.two) {
+                        if (!wait(&sh->q_full[0], q_use[0]++) || !wait(&sh->q_full[1], q_use[1]++)) break;
+                        if (!take(k_pos(0), k_fixed(0))) break;
+                        for (int w = 0; w < 2; ++w) {
+                            s_product(w, w, k_pos(0));
+                            mma_commit(&sh->s_full[w]);
+                        }
+                        free_stage(k_pos(0));
+                        for (int k = 0; ok && k < nt; ++k) {
+                            for (int w = 0; w < 2; ++w) {
+                                if (!wait(&sh->p_full[w], n2 + k)) break;
+                                if (k == 0 && !wait(&sh->o_free[w], pieces[w] + 1)) break;
+                                if (w == 0 && !take(v_pos(k), v_fixed(k))) break;
+                                tc_fence_after();
+                                pv_product(w, w, v_pos(k), k == 0);
+                                mma_commit(&sh->pv_done[w]);
+                                if (w == 1) free_stage(v_pos(k));
+                                if (k + 1 < nt) {
+                                    // overwrites P(k), which the product just issued reads:
+                                    // the tensor core takes them in this order
+                                    if (w == 0 && !take(k_pos(k + 1), k_fixed(k + 1))) break;
+                                    s_product(w, w, k_pos(k + 1));
+                                    mma_commit(&sh->s_full[w]);
+                                    if (w == 1) free_stage(k_pos(k + 1));
+                                } else {
+                                    mma_commit(&sh->q_empty[w]);
+                                }
+                            }
+                        }
+                        n2 += nt;
+                        ++pieces[0];
+                        ++pieces[1];
+                    } else {
+                        const int qs = ones++ & 1;
+                        if (!wait(&sh->q_full[qs], q_use[qs]++)) break;
+                        auto s_next = [&](int k) {
+                            if (!take(k_pos(k), k_fixed(k))) return;
+                            s_product(k & 1, qs, k_pos(k));
+                            mma_commit(&sh->s1_full[k & 1]);
+                            free_stage(k_pos(k));
+                        };
+                        s_next(0);
+                        for (int k = 0; ok && k < nt; ++k) {
+                            if (k + 1 < nt) {
+                                s_next(k + 1);  // overwrites P(k - 1): its product went first
+                            } else {
+                                mma_commit(&sh->q_empty[qs]);
+                            }
+                            if (!wait(&sh->p1_full[k & 1], n1[k & 1]++)) break;
+                            if (k == 0 && !wait(&sh->o_free[0], pieces[0] + 1)) break;
+                            if (!take(v_pos(k), v_fixed(k))) break;
+                            tc_fence_after();
+                            pv_product(0, k & 1, v_pos(k), k == 0);
+                            mma_commit(&sh->pv_done[0]);
+                            free_stage(v_pos(k));
+                        }
+                        ++pieces[0];
+                    }
+                    rc += 2 * nt;
+                }
+                mma_commit(&sh->drain);
+                mbar_wait_bounded(&sh->drain, 0, &sh->never, kWaitNs);
+            }
+        } else if (warp == 9) {
+            // ------------------------------------------------ TMA producer
+            const uint64_t pol = policy_evict_normal(), pol_first = policy_evict_first();
+            uint32_t pos = 0, q_use[2] = {0, 0}, ones = 0;
+            const int nb = kKeys / a.box;  // boxes per 64-d half of a cached tile
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t par) {
+                if (lane == 0 && !mbar_wait_bounded(bar, par & 1, abort_flag, kWaitNs)) {
+                    give_up();
+                    ok = false;
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                return ok;
+            };
+            for (bool has = wk.settle(); ok && has; has = wk.next()) {
+                const Piece& p = wk.p;
+                const int q0 = p.two ? 0 : ones++ & 1, q1 = p.two ? 1 : q0;
+                for (int s = q0; s <= q1; ++s) {
+                    if (!wait(&sh->q_empty[s], q_use[s] + 1)) break;
+                    ++q_use[s];
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&sh->q_full[s], (uint32_t)(a.tpq * a.grp * 128 * NH));
+                        for (int h = 0; h < NH; ++h)
+                            tma_load_4d(sQ + s * Shape::kTile + h * kHalfBytes, &tm_q, &sh->q_full[s], 64 * h,
+                                        p.g * a.grp, p.r.start + p.i0 + (s - q0) * a.tpq, 0, pol_first);
+                    }
+                }
+                // keys that only this item reads need not stay in L2
+                const uint64_t pol_kv = p.r.items == 1 ? pol_first : pol;
+                for (int t = p.t0; ok && t < p.t1; ++t) {
+                    for (int v = 0; v < 2; ++v, ++pos) {
+                        const uint32_t s = pos % NST;
+                        if (!wait(&sh->empty[s], pos / NST + 1)) break;
+                        unsigned char* dst = ring + s * Shape::kTile;
+                        if (lane == 0) mbar_arrive_expect_tx(&sh->full[s], Shape::kTile);
+                        __syncwarp();
+                        if (t >= p.r.kvt) {
+                            if (lane < NH)
+                                tma_load_4d(dst + lane * kHalfBytes, v ? &tm_vn : &tm_kn, &sh->full[s], 64 * lane,
+                                            p.g, p.r.start + (t - p.r.kvt) * kKeys, 0, pol);
+                            continue;
+                        }
+                        // one box per lane and step: `box` consecutive tokens of a page
+                        for (int x = lane; x < nb * NH; x += 32) {
+                            const int h = x / nb, row = (x - h * nb) * a.box;
+                            const int key = t * kKeys + row;
+                            int page = -1;  // a page past the cached keys, or a bad one, reads as zeros
+                            if (key < p.r.kv) {
+                                page = __ldg(a.page_table + (size_t)p.b * a.max_pages + key / a.P);
+                                if (page < 0 || page >= a.num_pages) {
+                                    raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
+                                    page = -1;
+                                }
+                            }
+                            tma_load_4d(dst + h * kHalfBytes + row * 128, v ? &tm_v : &tm_k, &sh->full[s], 64 * h,
+                                        p.g, key % a.P, page, pol_kv);
+                        }
+                    }
+                }
+            }
+            // drain: every copy has landed before the CTA may exit
+            if (lane == 0) {
+                for (uint32_t i = pos > NST ? pos - NST : 0; i < pos; ++i)
+                    mbar_wait_bounded(&sh->full[i % NST], (i / NST) & 1, &sh->never, kWaitNs);
+                for (int s = 0; s < 2; ++s)
+                    if (q_use[s]) mbar_wait_bounded(&sh->q_full[s], (q_use[s] - 1) & 1, &sh->never, kWaitNs);
+            }
+        } else if (warp == 10) {
+            // ------------------------------------------------ append
+            // this CTA's share of the new rows, each to its page, 16 bytes a lane
+            const int t0 = bad ? 0 : (int)((long long)a.T * blockIdx.x / gridDim.x);
+            const int t1 = bad ? 0 : (int)((long long)a.T * (blockIdx.x + 1) / gridDim.x);
+            if (t0 < t1) {
+                int lo = -1, hi = a.B;  // the last request that starts at or before t0
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (a.q_start[mid] <= t0) lo = mid; else hi = mid;
+                }
+                int b = lo;
+                for (int t = t0; t < t1; ++t) {
+                    while (b + 1 < a.B && a.q_start[b + 1] <= t) ++b;
+                    if (b < 0 || t >= a.q_start[b + 1]) continue;  // a row of no request
+                    const int start = a.q_start[b], kv = a.kv_len[b];
+                    if (chunk_tokens(a, kv, a.q_start[b + 1] - start) == 0) {
+                        if (lane == 0) raise_flag(a.err_flag, ISD_FLAG_CAPACITY);
+                        uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)t * a.Hq * D);
+                        for (int i = lane; i < a.Hq * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    const int at = kv + (t - start);
+                    const int page = a.page_table[(size_t)b * a.max_pages + at / a.P];
+                    if (page < 0 || page >= a.num_pages) {
+                        if (lane == 0) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
+                        continue;
+                    }
+                    const size_t dst = ((size_t)page * a.P + at % a.P) * a.Hkv * D, src = (size_t)t * a.Hkv * D;
+                    const uint4* ks = reinterpret_cast<const uint4*>(a.k_new + src);
+                    const uint4* vs = reinterpret_cast<const uint4*>(a.v_new + src);
+                    uint4* kd = reinterpret_cast<uint4*>(a.k_pool + dst);
+                    uint4* vd = reinterpret_cast<uint4*>(a.v_pool + dst);
+#pragma unroll 4
+                    for (int i = lane; i < a.Hkv * D / 8; i += 32) {
+                        kd[i] = __ldg(ks + i);
+                        vd[i] = __ldg(vs + i);
+                    }
+                }
+            }
+        } else {
+            // ------------------------------------------------ tiles that need a touch
+            // before a product may read them: rows that hold no key of the item
+            // are zeroed in V (0 * NaN would spoil the sum), the new tokens of a
+            // merged tile are put into their rows, and infinities and NaN in V
+            // rows that only some of the item's rows see are taken out and noted
+            // for the epilogue.
+            uint32_t rc = 0, fixes = 0, expect = 0;
+            (void)fixes;
+            int piece = 0;
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t par) {
+                bool good = mbar_wait_bounded(bar, par & 1, abort_flag, kWaitNs);
+                if (!good) give_up();
+                ok = __all_sync(0xffffffffu, good);
+                return ok;
+            };
+            auto done = [&](uint32_t s) {
+                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->fix[s]);
+            };
+            constexpr int kChunks = D / 8;          // 16-byte chunks of a row
+            constexpr int kRowsStep = 32 / kChunks;  // rows the warp covers at once
+            const int ch = lane % kChunks, r_in = lane / kChunks;
+            auto cell = [&](uint32_t s, int row) {
+                return reinterpret_cast<uint4*>(ring + s * Shape::kTile + (ch >> 3) * kHalfBytes + row * 128 +
+                                                (((ch & 7) ^ (row & 7)) << 4));
+            };
+            // notes what is not finite in this lane's chunk of token `tok` and returns the chunk without it
+            auto note = [&](uint4 w, int tok) {
+                uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t half = (x[i >> 1] >> (16 * (i & 1))) & 0xffffu;
+                    if ((half & 0x7f80u) != 0x7f80u) continue;
+                    const int kind = (half & 0x7fu) ? 2 : (half >> 15);
+                    atomicMin(&sh->bad_from[kind][ch * 8 + i], tok);
+                    x[i >> 1] &= ~(0xffffu << (16 * (i & 1)));
+                }
+                return make_uint4(x[0], x[1], x[2], x[3]);
+            };
+            // makes `bad_from` this piece's, once every earlier piece has read its own
+            auto claim = [&]() {
+                if (sh->bad_piece == piece) return true;
+                const uint64_t t_start = global_ns();
+                bool good = true;
+                while (*(volatile int*)&sh->epilogues < (int)expect) {
+                    if (*abort_flag || global_ns() - t_start > kWaitNs) {
+                        good = false;
+                        break;
+                    }
+                }
+                if (!good) give_up();
+                ok = __all_sync(0xffffffffu, good);
+                if (!ok) return false;
+                for (int i = lane; i < 3 * D; i += 32) (&sh->bad_from[0][0])[i] = 0x7fffffff;
+                __syncwarp();
+                if (lane == 0) *(volatile int*)&sh->bad_piece = piece;
+                __syncwarp();
+                return true;
+            };
+            for (bool has = wk.settle(); ok && has; has = wk.next()) {
+                const Piece& p = wk.p;
+                for (int t = p.t0; ok && t < p.t1; ++t) {
+                    const uint32_t kp = rc + 2 * (t - p.t0), vp = kp + 1;
+                    const uint32_t ks = kp % NST, vs = vp % NST;
+                    if (t < p.r.kvt) {
+                        const int m = p.r.kv - t * kKeys;  // cached keys of the tile
+                        if (m >= kKeys) continue;
+                        const int fresh = p.r.merged ? p.r.n : 0;
+                        if (fresh) {
+                            if (!wait(&sh->full[ks], kp / NST)) break;
+                            for (int i = r_in; i < fresh; i += kRowsStep)
+                                *cell(ks, m + i) = __ldg(reinterpret_cast<const uint4*>(
+                                                             a.k_new + ((size_t)(p.r.start + i) * a.Hkv + p.g) * D) + ch);
+                            done(ks);
+                        }
+                        if (!wait(&sh->full[vs], vp / NST)) break;
+                        for (int i0 = 0; i0 < fresh; i0 += kRowsStep) {
+                            const int i = i0 + r_in;
+                            uint4 w = make_uint4(0, 0, 0, 0);
+                            if (i < fresh)
+                                w = __ldg(reinterpret_cast<const uint4*>(
+                                              a.v_new + ((size_t)(p.r.start + i) * a.Hkv + p.g) * D) + ch);
+                            // the first new token is visible to every row
+                            const bool odd = i > 0 && (odd_pair(w.x) || odd_pair(w.y) || odd_pair(w.z) || odd_pair(w.w));
+                            if (__any_sync(0xffffffffu, odd)) {
+                                if (!claim()) break;
+                                if (odd) w = note(w, i);
+                            }
+                            if (i < fresh) *cell(vs, m + i) = w;
+                        }
+                        if (!ok) break;
+                        for (int row = m + fresh + r_in; row < kKeys; row += kRowsStep) *cell(vs, row) = make_uint4(0, 0, 0, 0);
+                        done(vs);
+                    } else {
+                        const int base = (t - p.r.kvt) * kKeys;
+                        if (base + kKeys <= p.i0 + 1) continue;  // every row sees all of it
+                        if (!wait(&sh->full[vs], vp / NST)) break;
+                        const int rows = min(kKeys, p.i1 - base);
+                        for (int r0 = max(0, p.i0 + 1 - base); r0 < rows; r0 += kRowsStep) {
+                            const int row = r0 + r_in;
+                            uint4 w = make_uint4(0, 0, 0, 0);
+                            if (row < rows) w = *cell(vs, row);
+                            const bool odd = odd_pair(w.x) || odd_pair(w.y) || odd_pair(w.z) || odd_pair(w.w);
+                            if (__any_sync(0xffffffffu, odd)) {
+                                if (!claim()) break;
+                                if (odd) *cell(vs, row) = note(w, base + row);
+                            }
+                        }
+                        if (!ok) break;
+                        for (int row = rows + r_in; row < kKeys; row += kRowsStep) *cell(vs, row) = make_uint4(0, 0, 0, 0);
+                        done(vs);
+                    }
+                }
+                rc += 2 * (p.t1 - p.t0);
+                expect += p.two ? 8 : 4;
+                ++piece;
+            }
+        }
+    } else {
+        setmaxnreg_inc<kRegsHigh>();
+        // ---------------------------------------------------- softmax and epilogue
+        const int wg = warp >> 2, rr = (warp & 3) * 32 + lane;  // row tile; row in it
+        const int tok = wg * a.tpq + rr / a.grp, head = rr % a.grp;
+        const bool row_used = rr < a.tpq * a.grp;
+        const uint32_t tm_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t tm_o = tm_lane + kTmemO + wg * D;
+        uint32_t n2 = 0, n1[2] = {0, 0}, pvs = 0;
+        int piece = 0;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t par) {
+            const bool good = mbar_wait_bounded(bar, par & 1, abort_flag, kWaitNs);
+            if (!good) give_up();
+            ok = __all_sync(0xffffffffu, good);
+            return ok;
+        };
+        // the piece's product k is done (its predecessor is waited for too: a
+        // barrier two phases behind would pass for done)
+        auto pv_wait = [&](int k) {
+            if (k > 0 && !wait(&sh->pv_done[wg], pvs + k - 1)) return false;
+            if (!wait(&sh->pv_done[wg], pvs + k)) return false;
+            tc_fence_after();
+            return true;
+        };
+        for (bool has = wk.settle(); ok && has; has = wk.next(), ++piece) {
+            const Piece& p = wk.p;
+            const int slot = wk.slot();
+            if (slot == 1 && threadIdx.x == 0) {
+                // CTAs that hold a part: this one to the owner of the item's last tile
+                const long long total_ = total, most = total_ / a.cost_max;
+                const int G = (int)min((long long)gridDim.x, max(most, 1ll));
+                const long long last_at = p.us + (long long)(p.nt - 1) * (p.two ? kCost2 : kCost1);
+                const int last = (int)(((last_at + 1) * G - 1) / total_);
+                ChunkCut* c = a.cuts + blockIdx.x;
+                c->g = p.g;
+                c->i0 = p.i0;
+                c->i1 = p.i1;
+                c->start = p.r.start;
+                c->parts = last - (int)blockIdx.x + 1;
+            }
+            if (wg == 1 && !p.two) continue;
+            const int i = p.i0 + tok;  // this row's token
+            const bool live = row_used && i < p.i1;
+            float m_ref = -INFINITY, l = 0.f;
+            const int nt = p.t1 - p.t0;
+            for (int k = 0; k < nt; ++k) {
+                const int t = p.t0 + k;
+                const int buf = p.two ? wg : k & 1;
+                if (p.two) {
+                    if (!wait(&sh->s_full[wg], n2)) break;
+                    ++n2;
+                } else {
+                    if (!wait(&sh->s1_full[buf], n1[buf])) break;
+                    ++n1[buf];
+                }
+                tc_fence_after();
+                float s[kKeys];
+                {
+                    uint32_t (&u)[kKeys] = reinterpret_cast<uint32_t(&)[kKeys]>(s);
+#pragma unroll
+                    for (int j = 0; j < kKeys; j += 32)
+                        tmem_ld_32x32b_x32(tm_lane + buf * kKeys + j, reinterpret_cast<uint32_t(&)[32]>(u[j]));
+                    tmem_ld_wait();
+                }
+                // keys of this tile that the row sees
+                int seen;
+                if (t < p.r.kvt) {
+                    seen = p.r.kv - t * kKeys;
+                    if (p.r.merged && seen <= kKeys) seen += i + 1;
+                } else {
+                    seen = i + 1 - (t - p.r.kvt) * kKeys;
+                }
+                if (!live) seen = 0;
+                if (__any_sync(0xffffffffu, seen < kKeys)) {
+#pragma unroll
+                    for (int j = 0; j < kKeys; ++j)
+                        if (j >= seen) s[j] = -INFINITY;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < kKeys; j += 4)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[j + e]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                const bool move = top > m_ref + 8.f;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float m_new = move ? top : m_ref;
+                    const float f = move ? ex2(m_ref - m_new) : 1.f;
+                    if (k > 0) {
+                        if (!pv_wait(k - 1)) break;
+#pragma unroll 1
+                        for (int j = 0; j < D; j += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tm_o + j, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(tm_o + j, o);
+                        }
+                        tmem_st_wait();
+                    }
+                    l *= f;
+                    m_ref = m_new;
+                }
+                const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                // weights are rounded to bf16 for the product with V; the sum
+                // takes them in 32 bits
+#pragma unroll
+                for (int j0 = 0; j0 < kKeys; j0 += 64) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int j = 0; j < 64; j += 2) {
+                        const float p0 = ex2(fmaf(s[j0 + j], a.scale_log2, -mu));
+                        const float p1 = ex2(fmaf(s[j0 + j + 1], a.scale_log2, -mu));
+                        sum[j & 2] += p0;
+                        sum[(j & 2) + 1] += p1;
+                        w[j >> 1] = pack_bf16(p0, p1);
+                    }
+                    tmem_st32(tm_lane + buf * kKeys + j0 / 2, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p.two ? &sh->p_full[wg] : &sh->p1_full[buf]);
+            }
+            if (!ok) break;
+            // ---- this piece's rows
+            if (!pv_wait(nt - 1)) break;
+            pvs += nt;
+            const bool odd = *(volatile int*)&sh->bad_piece == piece;
+            const float inv = 1.f / l;
+            __nv_bfloat16* orow = a.out + ((size_t)(p.r.start + i) * a.Hq + p.g * a.grp + head) * D;
+            float* part = a.part + ((size_t)blockIdx.x * 2 + max(slot, 0)) * (size_t)a.part_rows * (D + 2);
+            const int prow = wg * kTileRows + rr;
+            if (slot >= 0 && live) {
+                part[prow] = m_ref;
+                part[a.part_rows + prow] = l;
+            }
+            float* po = part + 2 * a.part_rows + prow;
+#pragma unroll
+            for (int j = 0; j < D; j += 32) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(tm_o + j, o);
+                tmem_ld_wait();
+                if (odd) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float v = __uint_as_float(o[e]);
+                        if (sh->bad_from[0][j + e] <= i) v += INFINITY;
+                        if (sh->bad_from[1][j + e] <= i) v -= INFINITY;
+                        if (sh->bad_from[2][j + e] <= i) v = NAN;
+                        o[e] = __float_as_uint(v);
+                    }
+                }
+                if (!live) continue;
+                if (slot >= 0) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) po[(size_t)(j + e) * a.part_rows] = __uint_as_float(o[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 w;
+                        w.x = pack_bf16(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+                        w.y = pack_bf16(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                        w.z = pack_bf16(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+                        w.w = pack_bf16(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+                        *reinterpret_cast<uint4*>(orow + j + e) = w;
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh->o_free[wg]);
+                atomicAdd(&sh->epilogues, 1);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Joins the parts of cut items, in CTA order: grid (CTAs, 32-row groups), a
+// lane per row, a warp per D / 8 dimensions.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
+    pdl_wait();
+    const ChunkCut cut = a.cuts[blockIdx.x];
+    if (cut.parts < 2) return;
+    const int lane = threadIdx.x & 31, d0 = (threadIdx.x >> 5) * (D / 8);
+    const int row = blockIdx.y * 32 + lane, rr = row % kTileRows;
+    const int i = cut.i0 + row / kTileRows * a.tpq + rr / a.grp;
+    if (rr >= a.tpq * a.grp || i >= cut.i1) return;
+    const size_t stride = (size_t)a.part_rows * (D + 2);
+    const float* first = a.part + ((size_t)blockIdx.x * 2 + 1) * stride + row;
+    // part k: the first one in slot 1 of its CTA, the others in slot 0 of theirs
+    auto part = [&](int k) { return k == 0 ? first : first + (size_t)(2 * k - 1) * stride; };
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int k = 0; k < cut.parts; ++k) m = fmaxf(m, *part(k));
+    if (m == -INFINITY) m = 0.f;
+    float l = 0.f, o[D / 8];
+#pragma unroll
+    for (int e = 0; e < D / 8; ++e) o[e] = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < cut.parts; ++k) {
+        const float* pk = part(k);
+        const float f = ex2(pk[0] - m);
+        l += f * pk[a.part_rows];
+        const float* po = pk + (size_t)(2 + d0) * a.part_rows;
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) o[e] += f * po[(size_t)e * a.part_rows];
+    }
+    const float inv = 1.f / l;
+    uint4* dst = reinterpret_cast<uint4*>(
+        a.out + ((size_t)(cut.start + i) * a.Hq + cut.g * a.grp + rr % a.grp) * D + d0);
+#pragma unroll
+    for (int e = 0; e < D / 8; e += 8)
+        dst[e / 8] = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                                pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+}
+
+bool encode_tiles(CUtensorMap* m, const void* ptr, uint64_t D, uint64_t heads, uint64_t rows, uint64_t outer,
+                  uint32_t box_heads, uint32_t box_rows) {
+    EncodeTiledFn fn = get_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t gd[4] = {D, heads, rows, outer};
+    const cuuint64_t gs[3] = {D * 2, heads * D * 2, rows * heads * D * 2};
+    const cuuint32_t bx[4] = {64, box_heads, box_rows, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), gd, gs, bx, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>
-cudaError_t launch_chunk_d(const ChunkArgs& a, cudaStream_t st) {
-    cudaError_t e = launch_kernel(false, chunk_append_kernel<D>, dim3((a.T + kAppendTokens - 1) / kAppendTokens),
-                                  dim3(32 * kAppendTokens), 0, st, a);
+cudaError_t launch_chunk_d(const ChunkArgs& a, const uint16_t* q, cudaStream_t st) {
+    static unsigned long long configured = 0;  // bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const long long warps = (long long)a.T * a.Hq;
-    return launch_kernel(false, chunk_attention_kernel<D>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, st, a);
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!(configured >> dev & 1ull)) {
+        // the register split assumes the launch allocation; a build that
+        // allots fewer registers would leave the increase waiting forever
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, chunk_kernel<D>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs < kLaunchRegs) {
+            set_error_detail("chunk attention: registers at launch below the warpgroup split");
+            return cudaErrorInvalidConfiguration;
+        }
+        e = cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)ChunkShape<D>::kSmem());
+        if (e != cudaSuccess) return e;
+        configured |= 1ull << dev;
+    }
+    CUtensorMap tq, tk, tv, tkn, tvn;
+    if (!encode_tiles(&tq, q, D, a.Hq, a.T, 1, a.grp, a.tpq) ||
+        !encode_tiles(&tk, a.k_pool, D, a.Hkv, a.P, a.num_pages, 1, a.box) ||
+        !encode_tiles(&tv, a.v_pool, D, a.Hkv, a.P, a.num_pages, 1, a.box) ||
+        !encode_tiles(&tkn, a.k_new, D, a.Hkv, a.T, 1, 1, kKeys) ||
+        !encode_tiles(&tvn, a.v_new, D, a.Hkv, a.T, 1, 1, kKeys)) {
+        set_error_detail("chunk attention: tensor map");
+        return cudaErrorInvalidValue;
+    }
+    const int grid = persistent_grid();
+    e = launch_kernel(false, chunk_kernel<D>, dim3(grid), dim3(kChunkThreads), ChunkShape<D>::kSmem(), st, tq, tk, tv,
+                      tkn, tvn, a);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(true, chunk_join_kernel<D>, dim3(grid, a.part_rows / 32), dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -159,22 +1024,28 @@ cudaError_t launch_chunk_attention(const isd_dims* d, int T, const uint16_t* q, 
     a.Hq = d->Hq;
     a.Hkv = d->Hkv;
     a.grp = d->Hq / d->Hkv;
+    a.tpq = kTileRows / a.grp;
     a.P = d->page_size;
+    a.box = kKeys;  // the largest power of two up to a tile that divides the page
+    while (d->page_size % a.box) a.box >>= 1;
     a.num_pages = d->num_pages;
     a.max_pages = d->max_pages_per_req;
+    a.cost_max = T > a.tpq ? kCost2 : kCost1;
+    a.part_rows = chunk_part_rows(d, T);
     a.scale_log2 = d->sm_scale * 1.4426950408889634f;
     a.page_table = page_table;
     a.kv_len = kv_len;
     a.q_start = q_start;
-    a.q = reinterpret_cast<const __nv_bfloat16*>(q);
     a.k_new = reinterpret_cast<const __nv_bfloat16*>(k_new);
     a.v_new = reinterpret_cast<const __nv_bfloat16*>(v_new);
     a.k_pool = reinterpret_cast<__nv_bfloat16*>(k_pool);
     a.v_pool = reinterpret_cast<__nv_bfloat16*>(v_pool);
     a.out = reinterpret_cast<__nv_bfloat16*>(out);
+    a.cuts = static_cast<ChunkCut*>(ws);
+    static_assert(sizeof(ChunkCut) == kChunkCutBytes, "workspace layout");
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + align_up((size_t)kMaxSMs * kChunkCutBytes, 256));
     a.err_flag = err_flag;
-    (void)ws;
-    return d->D == 64 ? launch_chunk_d<64>(a, st) : launch_chunk_d<128>(a, st);
+    return d->D == 64 ? launch_chunk_d<64>(a, q, st) : launch_chunk_d<128>(a, q, st);
 }
 
 }  // namespace isd

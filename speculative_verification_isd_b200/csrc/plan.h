@@ -83,11 +83,17 @@ inline size_t pages_ws_bytes(const isd_dims* d) {
            align_up((1 + 3 * (size_t)d->num_pages) * 4, 256);
 }
 
-// Workspace of isd_chunk_attention.
+// Workspace of isd_chunk_attention: per CTA a record of the work item it cuts,
+// then per CTA two partial results of up to chunk_part_rows rows (a maximum, a
+// sum and D values each): 256, or what T tokens of a KV group's heads need.
+constexpr size_t kChunkCutBytes = 32;
+inline int chunk_part_rows(const isd_dims* d, int T) {
+    const int grp = d->Hq / d->Hkv;
+    return T > 128 / grp ? 256 : (T * grp + 31) / 32 * 32;
+}
 inline size_t chunk_ws_bytes(const isd_dims* d, int T) {
-    (void)d;
-    (void)T;
-    return 256;
+    return align_up((size_t)kMaxSMs * kChunkCutBytes, 256) +
+           (size_t)kMaxSMs * 2 * chunk_part_rows(d, T) * (d->D + 2) * 4;
 }
 
 // SMs of the current device, capped at kMaxSMs (cached per device).  The one
