@@ -202,7 +202,8 @@ struct ChunkShared {
     int b, g, q;
     uint32_t tmem;
     int abort_flag, never;
-    int epilogues;   // finished by softmax warps
+    uint32_t issued;  // ring positions that the producer has begun to fill
+    uint32_t epilogues;  // finished by softmax warps
     int bad_piece;   // the piece whose `bad_from` holds, or -1
     int bad_from[3][D];  // first new token with +inf, -inf, NaN in dimension d of V
 };
@@ -280,6 +281,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         mbar_init(&sh->drain, 1);
         sh->abort_flag = sh->never = 0;
         sh->epilogues = 0;
+        sh->issued = 0;
         sh->bad_piece = -1;
         sh->b = a.B;
         fence_mbar_init();
@@ -536,7 +538,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         const uint32_t s = pos % NST;
                         if (!wait(&sh->empty[s], pos / NST + 1)) break;
                         unsigned char* dst = ring + s * Shape::kTile;
-                        if (lane == 0) mbar_arrive_expect_tx(&sh->full[s], Shape::kTile);
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&sh->full[s], Shape::kTile);
+                            *(volatile uint32_t*)&sh->issued = pos + 1;
+                        }
                         __syncwarp();
                         if (t >= p.r.kvt) {
                             if (lane < NH)
@@ -616,12 +621,29 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             // merged tile are put into their rows, and infinities and NaN in V
             // rows that only some of the item's rows see are taken out and noted
             // for the epilogue.
-            uint32_t rc = 0, fixes = 0, expect = 0;
-            (void)fixes;
+            uint32_t rc = 0, expect = 0;
             int piece = 0;
             bool ok = true;
-            auto wait = [&](uint64_t* bar, uint32_t par) {
-                bool good = mbar_wait_bounded(bar, par & 1, abort_flag, kWaitNs);
+            auto until = [&](auto&& ready) {
+                const uint64_t t_start = global_ns();
+                bool good = true;
+                for (uint32_t it = 1; !ready(); ++it) {
+                    __nanosleep(32);
+                    if ((it & 63) == 0 && (*abort_flag || global_ns() - t_start > kWaitNs)) {
+                        good = ready();
+                        break;
+                    }
+                }
+                if (!good) give_up();
+                ok = __all_sync(0xffffffffu, good);
+                return ok;
+            };
+            // the tile at ring position pos has landed.  This warp skips most
+            // positions, so it first waits until the producer is at this one: the
+            // barrier's phase is then the tile's, and stays it until the fix.
+            auto landed = [&](uint32_t pos) {
+                if (!until([&] { return *(volatile uint32_t*)&sh->issued > pos; })) return false;
+                const bool good = mbar_wait_bounded(&sh->full[pos % NST], (pos / NST) & 1, abort_flag, kWaitNs);
                 if (!good) give_up();
                 ok = __all_sync(0xffffffffu, good);
                 return ok;
@@ -654,17 +676,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             // makes `bad_from` this piece's, once every earlier piece has read its own
             auto claim = [&]() {
                 if (sh->bad_piece == piece) return true;
-                const uint64_t t_start = global_ns();
-                bool good = true;
-                while (*(volatile int*)&sh->epilogues < (int)expect) {
-                    if (*abort_flag || global_ns() - t_start > kWaitNs) {
-                        good = false;
-                        break;
-                    }
-                }
-                if (!good) give_up();
-                ok = __all_sync(0xffffffffu, good);
-                if (!ok) return false;
+                if (!until([&] { return *(volatile uint32_t*)&sh->epilogues >= expect; })) return false;
                 for (int i = lane; i < 3 * D; i += 32) (&sh->bad_from[0][0])[i] = 0x7fffffff;
                 __syncwarp();
                 if (lane == 0) *(volatile int*)&sh->bad_piece = piece;
@@ -681,13 +693,13 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         if (m >= kKeys) continue;
                         const int fresh = p.r.merged ? p.r.n : 0;
                         if (fresh) {
-                            if (!wait(&sh->full[ks], kp / NST)) break;
+                            if (!landed(kp)) break;
                             for (int i = r_in; i < fresh; i += kRowsStep)
                                 *cell(ks, m + i) = __ldg(reinterpret_cast<const uint4*>(
                                                              a.k_new + ((size_t)(p.r.start + i) * a.Hkv + p.g) * D) + ch);
                             done(ks);
                         }
-                        if (!wait(&sh->full[vs], vp / NST)) break;
+                        if (!landed(vp)) break;
                         for (int i0 = 0; i0 < fresh; i0 += kRowsStep) {
                             const int i = i0 + r_in;
                             uint4 w = make_uint4(0, 0, 0, 0);
@@ -708,7 +720,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     } else {
                         const int base = (t - p.r.kvt) * kKeys;
                         if (base + kKeys <= p.i0 + 1) continue;  // every row sees all of it
-                        if (!wait(&sh->full[vs], vp / NST)) break;
+                        if (!landed(vp)) break;
                         const int rows = min(kKeys, p.i1 - base);
                         for (int r0 = max(0, p.i0 + 1 - base); r0 < rows; r0 += kRowsStep) {
                             const int row = r0 + r_in;
@@ -747,10 +759,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             ok = __all_sync(0xffffffffu, good);
             return ok;
         };
-        // the piece's product k is done (its predecessor is waited for too: a
-        // barrier two phases behind would pass for done)
+        // the piece's product k is done; every product is waited for before the
+        // next one's weights are handed over, so the barrier is never two
+        // phases away
         auto pv_wait = [&](int k) {
-            if (k > 0 && !wait(&sh->pv_done[wg], pvs + k - 1)) return false;
             if (!wait(&sh->pv_done[wg], pvs + k)) return false;
             tc_fence_after();
             return true;
@@ -854,6 +866,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 }
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_st_wait();
+                if (k > 0 && !pv_wait(k - 1)) break;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p.two ? &sh->p_full[wg] : &sh->p1_full[buf]);
@@ -907,7 +920,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&sh->o_free[wg]);
-                atomicAdd(&sh->epilogues, 1);
+                atomicAdd(&sh->epilogues, 1u);
             }
         }
     }

@@ -145,6 +145,49 @@ def test_chunk(isd, name):
     c.upload().call().check()
 
 
+# enough work that every CTA walks several items of many key tiles
+LONG = {
+    "decode_long_pieces": (8, 8, 128, 16, [(613 * i) % 2900 for i in range(40)], [1] * 40),
+    "decode_d64_long_pieces": (16, 8, 64, 32, [(613 * i) % 2900 for i in range(40)], [1 + i % 3 for i in range(40)]),
+    "prompt_long_pieces": (16, 8, 64, 16, [0, 900], [900, 700]),
+    "prompt_d128_long_pieces": (32, 8, 128, 16, [300], [1100]),
+    "mixed_long_pieces": (8, 4, 128, 24, [(389 * i) % 2100 for i in range(30)],
+                          [1 if i % 3 else 40 + 9 * i for i in range(30)]),
+}
+
+
+@pytest.mark.parametrize("gain", [1.0, 20.0])
+@pytest.mark.parametrize("name", LONG)
+def test_chunk_long_pieces(isd, name, gain):
+    Hq, Hkv, D, P, ctx, n = LONG[name]
+    Chunk(isd, Hq, Hkv, D, P, ctx, n, seed=3, gain=gain).upload().call().check()
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_chunk_rising_scores_long_pieces(isd, n):
+    """The running maximum moves in every tile of pieces of many tiles."""
+    B, kv = 20, 1500
+    c = Chunk(isd, 8, 8, 128, 16, [kv] * B, [n] * B, seed=9)
+    c.q[:] = 1.0
+    ramp = (torch.arange(kv + n, dtype=torch.float32) / 64)[:, None, None].expand(-1, 8, 128).to(torch.bfloat16)
+    pos = np.arange(kv)
+    for b in range(B):
+        c.k_pool[c.table[b, pos // 16], pos % 16] = ramp[:kv]
+        c.k_new[b * n:(b + 1) * n] = ramp[kv:]
+    c.upload().call().check()
+
+
+def test_chunk_hidden_keys_long_pieces(isd):
+    """Non-finite values noted for one item do not reach the next ones."""
+    ctx, n = [700, 0, 300, 50] * 10, [30, 300, 3, 90] * 10
+    c = Chunk(isd, 8, 4, 64, 16, ctx, n, seed=21)
+    rng = np.random.default_rng(1)
+    odd = torch.tensor([float("nan"), float("inf"), float("-inf")])
+    for t in rng.integers(0, sum(n), 60):
+        c.v_new[t, rng.integers(0, 4), rng.integers(0, 64)] = odd[rng.integers(0, 3)]
+    c.upload().call().check()
+
+
 @pytest.mark.parametrize("gain,scale", [(30.0, 0.0), (1.0, 0.5), (1.0, 1e-3)])
 def test_chunk_scores_far_apart(isd, gain, scale):
     """Row maxima that move by more than 2^8 between tiles; flat scores."""
