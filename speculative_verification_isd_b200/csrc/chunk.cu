@@ -933,45 +933,68 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     }
 }
 
-// Joins the parts of cut items, in CTA order: grid (CTAs, 32-row groups), a
-// lane per row, a warp per D / 8 dimensions.
+// Joins the parts of cut items, in CTA order: grid (CTAs, 32-row groups,
+// slices of the dimensions), a lane per row; the 8 warps take the parts in turn,
+// merge their own, and meet in shared memory.
+constexpr int kJoinWarps = 8, kJoinDims = 16;
 template <int D>
-__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
+    __shared__ float red[kJoinWarps][kJoinDims + 2][32];
     pdl_wait();
     const ChunkCut cut = a.cuts[blockIdx.x];
     if (cut.parts < 2) return;
-    const int lane = threadIdx.x & 31, d0 = (threadIdx.x >> 5) * (D / 8);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.y * 32 + lane, rr = row % kTileRows;
     const int i = cut.i0 + row / kTileRows * a.tpq + rr / a.grp;
-    if (rr >= a.tpq * a.grp || i >= cut.i1) return;
+    const bool live = rr < a.tpq * a.grp && i < cut.i1;
+    if (!__any_sync(0xffffffffu, live)) return;  // the same lanes in every warp
     const size_t stride = (size_t)a.part_rows * (D + 2);
     const float* first = a.part + ((size_t)blockIdx.x * 2 + 1) * stride + row;
-    // part k: the first one in slot 1 of its CTA, the others in slot 0 of theirs
-    auto part = [&](int k) { return k == 0 ? first : first + (size_t)(2 * k - 1) * stride; };
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int k = 0; k < cut.parts; ++k) m = fmaxf(m, *part(k));
-    if (m == -INFINITY) m = 0.f;
-    float l = 0.f, o[D / 8];
+    __nv_bfloat16* out = a.out + ((size_t)(cut.start + i) * a.Hq + cut.g * a.grp + rr % a.grp) * D;
+    for (int d0 = blockIdx.z * kJoinDims; d0 < D; d0 += gridDim.z * kJoinDims) {
+        float m = -INFINITY, l = 0.f, o[kJoinDims];
 #pragma unroll
-    for (int e = 0; e < D / 8; ++e) o[e] = 0.f;
-#pragma unroll 2
-    for (int k = 0; k < cut.parts; ++k) {
-        const float* pk = part(k);
-        const float f = ex2(pk[0] - m);
-        l += f * pk[a.part_rows];
-        const float* po = pk + (size_t)(2 + d0) * a.part_rows;
+        for (int e = 0; e < kJoinDims; ++e) o[e] = 0.f;
+        if (live) {
+            for (int k = warp; k < cut.parts; k += kJoinWarps) {
+                // part k: the first one in slot 1 of its CTA, the others in slot 0 of theirs
+                const float* pk = k == 0 ? first : first + (size_t)(2 * k - 1) * stride;
+                const float* po = pk + (size_t)(2 + d0) * a.part_rows;
+                const float mk = pk[0], lk = pk[a.part_rows];
+                float ok[kJoinDims];
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e) o[e] += f * po[(size_t)e * a.part_rows];
+                for (int e = 0; e < kJoinDims; ++e) ok[e] = po[(size_t)e * a.part_rows];
+                const float mn = fmaxf(m, mk), mu = mn == -INFINITY ? 0.f : mn;
+                const float f0 = ex2(m - mu), f1 = ex2(mk - mu);
+                l = l * f0 + lk * f1;
+#pragma unroll
+                for (int e = 0; e < kJoinDims; ++e) o[e] = o[e] * f0 + ok[e] * f1;
+                m = mn;
+            }
+        }
+        red[warp][0][lane] = m;
+        red[warp][1][lane] = l;
+#pragma unroll
+        for (int e = 0; e < kJoinDims; ++e) red[warp][2 + e][lane] = o[e];
+        __syncthreads();
+        // two dimensions per thread
+        const int used = min(cut.parts, kJoinWarps);
+        float top = -INFINITY;
+        for (int w = 0; w < used; ++w) top = fmaxf(top, red[w][0][lane]);
+        if (top == -INFINITY) top = 0.f;
+        float sum = 0.f, x = 0.f, y = 0.f;
+        for (int w = 0; w < used; ++w) {
+            const float f = ex2(red[w][0][lane] - top);
+            sum += f * red[w][1][lane];
+            x += f * red[w][2 + 2 * warp][lane];
+            y += f * red[w][3 + 2 * warp][lane];
+        }
+        const float inv = 1.f / sum;
+        if (live) *reinterpret_cast<uint32_t*>(out + d0 + 2 * warp) = pack_bf16(x * inv, y * inv);
+        __syncthreads();
     }
-    const float inv = 1.f / l;
-    uint4* dst = reinterpret_cast<uint4*>(
-        a.out + ((size_t)(cut.start + i) * a.Hq + cut.g * a.grp + rr % a.grp) * D + d0);
-#pragma unroll
-    for (int e = 0; e < D / 8; e += 8)
-        dst[e / 8] = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                                pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
 }
+static_assert(kJoinDims == 2 * kJoinWarps, "two dimensions per thread");
 
 bool encode_tiles(CUtensorMap* m, const void* ptr, uint64_t D, uint64_t heads, uint64_t rows, uint64_t outer,
                   uint32_t box_heads, uint32_t box_rows) {
@@ -1021,7 +1044,9 @@ cudaError_t launch_chunk_d(const ChunkArgs& a, const uint16_t* q, cudaStream_t s
     e = launch_kernel(false, chunk_kernel<D>, dim3(grid), dim3(kChunkThreads), ChunkShape<D>::kSmem(), st, tq, tk, tv,
                       tkn, tvn, a);
     if (e != cudaSuccess) return e;
-    return launch_kernel(true, chunk_join_kernel<D>, dim3(grid, a.part_rows / 32), dim3(256), 0, st, a);
+    // about 8 blocks per CTA of the cut, whatever the rows
+    const int groups = a.part_rows / 32, slices = groups >= 8 ? 1 : groups >= 4 ? 2 : groups >= 2 ? 4 : D / kJoinDims;
+    return launch_kernel(true, chunk_join_kernel<D>, dim3(grid, groups, slices), dim3(32 * kJoinWarps), 0, st, a);
 }
 
 }  // namespace
