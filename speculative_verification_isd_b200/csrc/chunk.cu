@@ -22,9 +22,11 @@
 //    (P overwrites S as bf16); a softmax thread owns one row, its maximum and
 //    sum live in registers, and O is rescaled only when a maximum grows by
 //    more than 2^8;
-//  * a prompt item keeps two tiles in flight (one warpgroup each), so that one
-//    tile's softmax runs under the other's products; an item of at most 128 rows
-//    (decoding) double-buffers S instead;
+//  * two warpgroups of softmax threads, each with its S and O, so that one's
+//    softmax runs under the other's products: in an item of two tiles each
+//    has a tile, in an item of one they take the key tiles in turn and add up
+//    their O at the end; with at most 32 rows (decoding) the rows are put
+//    into Q four times and each warp takes a quarter of a tile's keys;
 //  * every wait is bounded (about 2 s): on time-out the CTA raises
 //    ISD_FLAG_WAIT_TIMEOUT, all roles leave their loops, copies and MMAs in
 //    flight are drained and TMEM is released.
@@ -65,7 +67,8 @@ struct ChunkCut {
 };
 
 struct ChunkArgs {
-    int B, T, Hq, Hkv, grp, tpq, P, box, num_pages, max_pages;
+    int B, T, Hq, Hkv, grp, P, box, num_pages, max_pages;
+    int tpq, tps;   // tokens of a tile of 128 rows, and of one of 32
     int cost_max;   // the dearest key tile that this T allows
     int part_rows;  // rows of a partial result
     float scale_log2;
@@ -87,7 +90,7 @@ struct ChunkArgs {
 ISD_DEVINL int chunk_tokens(const ChunkArgs& a, int kv, int n) {
     if (kv < 0) return 0;
     const long long t = (long long)kv + n;
-    return (t + a.P - 1) / a.P > a.max_pages ? 0 : n;
+    return t > (long long)a.max_pages * a.P ? 0 : n;
 }
 
 // A request as the partition sees it.
@@ -98,96 +101,52 @@ struct Request {
     int items;    // per KV head
 };
 
-ISD_DEVINL Request request_of(const ChunkArgs& a, int b) {
+ISD_DEVINL Request request_of(const ChunkArgs& a, int start, int end, int kv) {
     Request r;
-    r.start = a.q_start[b];
-    r.kv = a.kv_len[b];
-    r.n = chunk_tokens(a, r.kv, a.q_start[b + 1] - r.start);
-    r.kvt = (max(r.kv, 0) + kKeys - 1) / kKeys;
-    r.merged = r.n <= kMergeTokens && r.n <= r.kvt * kKeys - r.kv;
+    r.start = start;
+    r.kv = kv;
+    r.n = chunk_tokens(a, kv, end - start);
+    r.kvt = (max(kv, 0) + kKeys - 1) / kKeys;
+    r.merged = r.n <= kMergeTokens && r.n <= r.kvt * kKeys - kv;
     r.items = (r.n + 2 * a.tpq - 1) / (2 * a.tpq);
     return r;
 }
 
-ISD_DEVINL int item_end(const ChunkArgs& a, const Request& r, int q) { return min(r.n, (q + 1) * 2 * a.tpq); }
-ISD_DEVINL bool item_two(const ChunkArgs& a, const Request& r, int q) {
-    return item_end(a, r, q) - q * 2 * a.tpq > a.tpq;
-}
-ISD_DEVINL int item_tiles(const ChunkArgs& a, const Request& r, int q) {
-    return r.kvt + (r.merged ? 0 : (item_end(a, r, q) + kKeys - 1) / kKeys);
-}
-ISD_DEVINL int item_cost(const ChunkArgs& a, const Request& r, int q) {
-    const int nt = item_tiles(a, r, q);
-    return item_two(a, r, q) ? kCost2 * nt + kEnds2 : kCost1 * nt + kEnds1;
-}
-ISD_DEVINL long long head_cost(const ChunkArgs& a, const Request& r) {
-    long long c = 0;
-    for (int q = 0; q < r.items; ++q) c += item_cost(a, r, q);
-    return c;
-}
-
-// This CTA's share of one item: key tiles [t0, t1).
-struct Piece {
-    int b, g, q;
-    long long us;  // the item's start on the partition axis
-    Request r;
+struct Item {
+    int i0, i1;  // its tokens
     bool two;
-    int nt, cost, t0, t1;
-    int i0, i1;    // its tokens
+    int nt, w, cost;  // key tiles, cost of one, of all
 };
 
-// Walks the CTA's range [my0, my1); the order is request, KV head, item.
-struct Walker {
-    const ChunkArgs& a;
-    long long my0, my1;
-    Piece p;
+ISD_DEVINL Item item_of(const ChunkArgs& a, const Request& r, int q) {
+    Item it;
+    it.i0 = q * 2 * a.tpq;
+    it.i1 = min(r.n, it.i0 + 2 * a.tpq);
+    it.two = it.i1 - it.i0 > a.tpq;
+    it.nt = r.kvt + (r.merged ? 0 : (it.i1 + kKeys - 1) / kKeys);
+    it.w = it.two ? kCost2 : kCost1;
+    it.cost = it.w * it.nt + (it.two ? kEnds2 : kEnds1);
+    return it;
+}
 
-    ISD_DEVINL void fill() {
-        p.two = item_two(a, p.r, p.q);
-        p.nt = item_tiles(a, p.r, p.q);
-        p.cost = item_cost(a, p.r, p.q);
-        p.i0 = p.q * 2 * a.tpq;
-        p.i1 = item_end(a, p.r, p.q);
-        const int w = p.two ? kCost2 : kCost1;
-        const long long lo = my0 - p.us, hi = my1 - p.us;
-        p.t0 = lo <= 0 ? 0 : (int)((lo + w - 1) / w);
-        p.t1 = (int)min((long long)p.nt, (hi + w - 1) / w);
-    }
-    ISD_DEVINL void step() {
-        p.us += p.cost;
-        if (++p.q < p.r.items) return;
-        p.q = 0;
-        if (++p.g < a.Hkv) return;
-        p.g = 0;
-        do {
-            if (++p.b >= a.B) return;
-            p.r = request_of(a, p.b);
-        } while (p.r.items == 0);
-    }
-    // to the first piece with a tile, starting from the item the walker is at
-    ISD_DEVINL bool settle() {
-        while (p.b < a.B && p.us < my1) {
-            fill();
-            if (p.t0 < p.t1) return true;
-            step();
-        }
-        return false;
-    }
-    ISD_DEVINL bool next() {
-        step();
-        return settle();
-    }
-    // a piece that is not the whole item leaves a partial: slot 0 when the
-    // item began before this range, 1 when it goes on past it
-    ISD_DEVINL int slot() const { return p.t0 > 0 ? 0 : p.t1 < p.nt ? 1 : -1; }
+// This CTA's share of one item, as its roles see it.
+enum { kTwo = 0, kOne = 1, kQuad = 2 };
+struct Piece {
+    int b, g, start, kv, kvt;
+    int i0, i1, t0, t1;  // tokens; key tiles (none: no more pieces)
+    int mode;            // two row tiles, one, or one of at most 32 rows
+    int slot;            // of the partial result, -1 for a whole item
+    int merged;          // the new tokens lie in the last cached tile
 };
+constexpr int kPieces = 16;  // pieces that the roles may lie apart
 
 template <int D>
 struct ChunkShape {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = kHalves * kHalfBytes;  // bytes of a Q, K or V tile
     static constexpr int kStages = D == 128 ? 5 : 10;   // ring of K and V tiles
-    static constexpr size_t kSmem() { return 1024 + (size_t)(2 + kStages) * kTile + 2048; }
+    static constexpr int kControl = 3072;
+    static constexpr size_t kSmem() { return (size_t)(2 + kStages) * kTile + kControl; }
 };
 
 template <int D>
@@ -195,16 +154,18 @@ struct ChunkShared {
     static constexpr int S = ChunkShape<D>::kStages;
     uint64_t full[S], empty[S], fix[S];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2];    // two-tile items: by tile
-    uint64_t s1_full[2], p1_full[2];  // one-tile items: by S buffer
-    uint64_t pv_done[2], o_free[2], drain;
-    long long my0, my1, us;
-    int b, g, q;
+    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];  // by softmax warpgroup
+    uint64_t meet, drain;
+    Piece pieces[kPieces];
+    long long my0, total;
+    int len, rel, b, g, q;
     uint32_t tmem;
     int abort_flag, never;
-    uint32_t issued;  // ring positions that the producer has begun to fill
-    uint32_t epilogues;  // finished by softmax warps
-    int bad_piece;   // the piece whose `bad_from` holds, or -1
+    uint32_t published;  // pieces written by the producer
+    uint32_t issued;     // ring positions that the producer has begun to fill
+    uint32_t fixed;      // pieces that the fixing warp is done with
+    uint32_t epilogues[2];  // finished by the warps of a softmax warpgroup (4 a piece)
+    int bad_piece;       // the piece whose `bad_from` holds, or -1
     int bad_from[3][D];  // first new token with +inf, -inf, NaN in dimension d of V
 };
 
@@ -212,6 +173,26 @@ ISD_DEVINL float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// two 32-bit operations at once
+ISD_DEVINL unsigned long long pair(float lo, float hi) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+ISD_DEVINL void unpair(unsigned long long v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+ISD_DEVINL unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+ISD_DEVINL unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 ISD_DEVINL void tmem_st32(uint32_t taddr, const uint32_t* r) {
@@ -224,6 +205,11 @@ ISD_DEVINL void tmem_st32(uint32_t taddr, const uint32_t* r) {
         "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+ISD_DEVINL void tmem_ld8(uint32_t taddr, uint32_t* r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
 
 // D(tmem) (+)= A(tmem) * B(smem desc), kind::f16
 ISD_DEVINL void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -233,6 +219,9 @@ ISD_DEVINL void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uin
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+ISD_DEVINL void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
 
 ISD_DEVINL uint64_t policy_evict_normal() {
     uint64_t p;
@@ -240,24 +229,28 @@ ISD_DEVINL uint64_t policy_evict_normal() {
     return p;
 }
 
+ISD_DEVINL void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+
 // Whether one of two packed bf16 is infinite or NaN.
 ISD_DEVINL bool odd_pair(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
 
+ISD_DEVINL uint32_t peek(const uint32_t* p) { return *(const volatile uint32_t*)p; }
+
 template <int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
-chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kn,
-             const __grid_constant__ CUtensorMap tm_vn, const __grid_constant__ ChunkArgs a) {
+chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qs,
+             const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+             const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_vn,
+             const __grid_constant__ ChunkArgs a) {
     using namespace sm100;
     using Shape = ChunkShape<D>;
     constexpr int NH = Shape::kHalves, NST = Shape::kStages;
     constexpr uint32_t kTmemCols = 512, kTmemO = 256;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* sQ = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                         ~uintptr_t(1023));
+    extern __shared__ __align__(1024) unsigned char smem_raw[];  // there is no other shared memory
+    unsigned char* sQ = smem_raw;
     unsigned char* ring = sQ + 2 * Shape::kTile;
     ChunkShared<D>* sh = reinterpret_cast<ChunkShared<D>*>(ring + NST * Shape::kTile);
-    static_assert(sizeof(ChunkShared<D>) <= 2048, "control block");
+    static_assert(sizeof(ChunkShared<D>) <= Shape::kControl, "control block");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_trigger();
 
@@ -272,95 +265,100 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             mbar_init(&sh->q_full[i], 1);
             mbar_init(&sh->q_empty[i], 1);
             mbar_init(&sh->s_full[i], 1);
-            mbar_init(&sh->s1_full[i], 1);
             mbar_init(&sh->p_full[i], 4);
-            mbar_init(&sh->p1_full[i], 4);
             mbar_init(&sh->pv_done[i], 1);
-            mbar_init(&sh->o_free[i], 4);
+            mbar_init(&sh->o_free[i], 8);
         }
+        mbar_init(&sh->meet, 8);
         mbar_init(&sh->drain, 1);
         sh->abort_flag = sh->never = 0;
-        sh->epilogues = 0;
-        sh->issued = 0;
+        sh->published = sh->issued = sh->fixed = sh->epilogues[0] = sh->epilogues[1] = 0;
         sh->bad_piece = -1;
         sh->b = a.B;
         fence_mbar_init();
+        a.cuts[blockIdx.x].parts = 0;
+    }
+    if (warp == 9 && lane == 0) {
         prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_qs);
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
         prefetch_tmap(&tm_kn);
         prefetch_tmap(&tm_vn);
-        a.cuts[blockIdx.x].parts = 0;
     }
     if (warp == 8) {
         tmem_alloc(&sh->tmem, kTmemCols);
         tmem_relinquish();
     }
     bool bad = false;
-    long long total = 0;
-    // costs of the requests, summed in order: the whole first, then again up to
-    // the request that holds this CTA's first position
     {
+        // costs of the requests, summed in order: a thread per request, and
+        // when there are more than threads, once for the total and again up to
+        // the request that holds this CTA's first position
         long long* wsum = reinterpret_cast<long long*>(ring);  // 12 warp sums (the ring is not in use yet)
-        const long long none = -1;
-        long long my0 = none, my1 = none;
-        for (int pass = 0; pass < 2; ++pass) {
-            long long run = 0;
-            for (int b0 = 0; b0 < a.B; b0 += kChunkThreads) {
-                const int b = b0 + (int)threadIdx.x;
-                long long c = 0;
-                Request r = {};
-                if (b < a.B) {
-                    const int s = a.q_start[b], e = a.q_start[b + 1];
-                    if (s < 0 || e < s || e > a.T) bad = true;
-                    else {
-                        r = request_of(a, b);
-                        c = head_cost(a, r) * a.Hkv;
-                    }
-                }
-                long long incl = c;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const long long v = __shfl_up_sync(0xffffffffu, incl, off);
-                    if (lane >= off) incl += v;
-                }
-                __syncthreads();
-                if (lane == 31) wsum[warp] = incl;
-                __syncthreads();
-                long long before = run;
-                for (int w = 0; w < kChunkThreads / 32; ++w) {
-                    if (w < warp) before += wsum[w];
-                    run += wsum[w];
-                }
-                before += incl - c;
-                if (pass == 1 && my0 < my1 && before <= my0 && my0 < before + c) {
-                    long long rem = my0 - before;
-                    const long long hc = c / a.Hkv;
-                    const int g = (int)(rem / hc);
-                    rem -= g * hc;
-                    int q = 0;
-                    for (int w; (w = item_cost(a, r, q)) <= rem; ++q) rem -= w;
-                    sh->b = b;
-                    sh->g = g;
-                    sh->q = q;
-                    sh->us = my0 - rem;
+        long long run = 0, before = 0, head = 0;
+        Request r = {};
+        auto pass = [&](int b) {
+            head = 0;
+            if (b < a.B) {
+                const int s = a.q_start[b], e = a.q_start[b + 1], kv = a.kv_len[b];
+                if (s < 0 || e < s || e > a.T) {
+                    bad = true;
+                } else {
+                    r = request_of(a, s, e, kv);
+                    for (int q = 0; q < r.items; ++q) head += item_of(a, r, q).cost;
                 }
             }
-            if (pass == 0) {
-                total = run;
-                const long long most = total / a.cost_max;  // every CTA between an item's ends has a tile of it
-                const int G = (int)min((long long)gridDim.x, max(most, 1ll));
-                const bool mine = (int)blockIdx.x < G;
-                my0 = mine ? total * blockIdx.x / G : 0;
-                my1 = mine ? total * (blockIdx.x + 1) / G : 0;
-                if (threadIdx.x == 0) {
-                    sh->my0 = my0;
-                    sh->my1 = my1;
-                }
+            const long long c = head * a.Hkv;
+            long long incl = c;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += v;
+            }
+            __syncthreads();
+            if (lane == 31) wsum[warp] = incl;
+            __syncthreads();
+            before = run + incl - c;
+            for (int w = 0; w < kChunkThreads / 32; ++w) {
+                if (w < warp) before += wsum[w];
+                run += wsum[w];
+            }
+        };
+        for (int b0 = 0; b0 < a.B; b0 += kChunkThreads) pass(b0 + (int)threadIdx.x);
+        const long long total = run;
+        const long long most = total / a.cost_max;  // every CTA between an item's ends has a tile of it
+        const int G = (int)min((long long)gridDim.x, max(most, 1ll));
+        const bool mine = (int)blockIdx.x < G;
+        const long long my0 = mine ? total * blockIdx.x / G : 0, my1 = mine ? total * (blockIdx.x + 1) / G : 0;
+        if (threadIdx.x == 0) {
+            sh->my0 = my0;
+            sh->total = total;
+            sh->len = (int)(my1 - my0);
+        }
+        auto locate = [&](int b) {
+            if (my0 >= my1 || my0 < before || my0 >= before + head * a.Hkv) return;
+            long long rem = my0 - before;
+            const int g = (int)(rem / head);
+            rem -= g * head;
+            int q = 0;
+            for (int w; (w = item_of(a, r, q).cost) <= rem; ++q) rem -= w;
+            sh->b = b;
+            sh->g = g;
+            sh->q = q;
+            sh->rel = -(int)rem;
+        };
+        if (a.B <= kChunkThreads) {
+            locate(threadIdx.x);
+        } else {
+            run = 0;
+            for (int b0 = 0; b0 < a.B; b0 += kChunkThreads) {
+                pass(b0 + (int)threadIdx.x);
+                locate(b0 + (int)threadIdx.x);
             }
         }
     }
-    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    proxy_fence();
     tc_fence_before();
     bad = __syncthreads_or(bad);
     tc_fence_after();
@@ -371,12 +369,29 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         *abort_flag = 1;
         raise_flag(a.err_flag, ISD_FLAG_WAIT_TIMEOUT);
     };
-    Walker wk{a, sh->my0, sh->my1, {}};
-    wk.p.b = bad ? a.B : sh->b;
-    wk.p.g = sh->g;
-    wk.p.q = sh->q;
-    wk.p.us = sh->us;
-    if (wk.p.b < a.B) wk.p.r = request_of(a, wk.p.b);
+    // waits on a counter in shared memory; every lane that asks gets the answer
+    auto until = [&](const uint32_t* counter, uint32_t least) {
+        if (peek(counter) >= least) return true;
+        const uint64_t t_start = global_ns();
+        for (uint32_t it = 1; peek(counter) < least; ++it) {
+            __nanosleep(20);
+            if ((it & 63) == 0 && (*abort_flag || global_ns() - t_start > kWaitNs)) {
+                give_up();
+                return false;
+            }
+        }
+        return true;
+    };
+    // piece number n, once it is published
+    auto pieces_done = [&](uint32_t n) {  // the softmax warps are past n pieces
+        return until(&sh->epilogues[0], 4 * n) && until(&sh->epilogues[1], 4 * n);
+    };
+    auto piece_at = [&](uint32_t n, Piece& p) {
+        if (!until(&sh->published, n + 1)) return false;
+        __threadfence_block();
+        p = sh->pieces[n % kPieces];
+        return p.t0 < p.t1;
+    };
 
     if (warp >= 8) {
         setmaxnreg_dec<kRegsLow>();
@@ -390,10 +405,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 // V as an operand with its dimensions contiguous: the two 64-d
                 // halves are kHalfBytes apart, 8-key groups 1024 bytes
                 const uint64_t dv = (dk & ~(0x3FFFull << 16)) | ((uint64_t)(kHalfBytes >> 4) << 16);
-                uint32_t rc = 0;             // ring position of the piece's first K tile
-                uint32_t fixes = 0;          // per stage: parity of the next fix
-                uint32_t q_use[2] = {0, 0}, n2 = 0, n1[2] = {0, 0}, pieces[2] = {0, 0};
-                uint32_t ones = 0;
+                uint32_t rc = 0;     // ring position of the piece's first K tile
+                uint32_t fixes = 0;  // per stage: parity of the next fix
+                uint32_t q_use[2] = {0, 0}, p_use[2] = {0, 0}, ones = 0;
                 bool ok = true;
                 auto wait = [&](uint64_t* bar, uint32_t par) {
                     if (ok && !mbar_wait_bounded(bar, par & 1, abort_flag, kWaitNs)) {
@@ -412,92 +426,83 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     tc_fence_after();
                     return true;
                 };
-                auto s_product = [&](int buf, int qs, uint32_t pos) {
+                auto free_stage = [&](uint32_t pos) { mma_commit(&sh->empty[pos % NST]); };
+                auto s_product = [&](int w, int qs, uint32_t pos) {
                     const uint32_t k_off = (pos % NST) * Shape::kTile, q_off = (uint32_t)qs * Shape::kTile;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t in = (uint32_t)((kk >> 2) * kHalfBytes + (kk & 3) * 32);
-                        mma_f16_ss(tmem + buf * kKeys, dq + ((q_off + in) >> 4), dk + ((k_off + in) >> 4), idesc_s,
+                        mma_f16_ss(tmem + w * kKeys, dq + ((q_off + in) >> 4), dk + ((k_off + in) >> 4), idesc_s,
                                    kk != 0);
                     }
+                    mma_commit(&sh->s_full[w]);
                 };
-                auto pv_product = [&](int o, int buf, uint32_t pos, bool first) {
+                auto pv_product = [&](int w, uint32_t pos, bool first) {
                     const uint32_t v_off = (pos % NST) * Shape::kTile;
 #pragma unroll
                     for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_f16_ts(tmem + kTmemO + o * D, tmem + buf * kKeys + kk * 8, dv + ((v_off + kk * 2048) >> 4),
+                        mma_f16_ts(tmem + kTmemO + w * D, tmem + w * kKeys + kk * 8, dv + ((v_off + kk * 2048) >> 4),
                                    idesc_o, !(first && kk == 0));
+                    mma_commit(&sh->pv_done[w]);
                 };
-                for (bool has = wk.settle(); ok && has; has = wk.next()) {
-                    const Piece& p = wk.p;
+                Piece p;
+                for (uint32_t n = 0; ok && piece_at(n, p); ++n) {
                     const int nt = p.t1 - p.t0;
                     // which tiles the fixing warp touches first
-                    auto k_fixed = [&](int k) { return p.r.merged && p.t0 + k == p.r.kvt - 1; };
+                    auto k_fixed = [&](int k) { return p.merged && p.t0 + k == p.kvt - 1; };
                     auto v_fixed = [&](int k) {
                         const int t = p.t0 + k;
-                        if (t < p.r.kvt) return (t + 1) * kKeys > p.r.kv;
-                        return (t + 1 - p.r.kvt) * kKeys > p.i0 + 1;
+                        if (t < p.kvt) return (t + 1) * kKeys > p.kv;
+                        return (t + 1 - p.kvt) * kKeys > p.i0 + 1;
                     };
                     auto k_pos = [&](int k) { return rc + 2 * k; };
                     auto v_pos = [&](int k) { return rc + 2 * k + 1; };
-                    auto free_stage = [&](uint32_t pos) { mma_commit(&sh->empty[pos % NST]); };
-                    if (p.two) {
+                    // S(k + ...) overwrites P(k), which the product issued before it
+                    // reads: the tensor core takes them in this order
+                    if (p.mode == kTwo) {
                         if (!wait(&sh->q_full[0], q_use[0]++) || !wait(&sh->q_full[1], q_use[1]++)) break;
                         if (!take(k_pos(0), k_fixed(0))) break;
-                        for (int w = 0; w < 2; ++w) {
-                            s_product(w, w, k_pos(0));
-                            mma_commit(&sh->s_full[w]);
-                        }
+                        s_product(0, 0, k_pos(0));
+                        s_product(1, 1, k_pos(0));
                         free_stage(k_pos(0));
                         for (int k = 0; ok && k < nt; ++k) {
+#pragma unroll 1
                             for (int w = 0; w < 2; ++w) {
-                                if (!wait(&sh->p_full[w], n2 + k)) break;
-                                if (k == 0 && !wait(&sh->o_free[w], pieces[w] + 1)) break;
+                                if (!wait(&sh->p_full[w], p_use[w]++)) break;
+                                if (k == 0 && !wait(&sh->o_free[w], n + 1)) break;
                                 if (w == 0 && !take(v_pos(k), v_fixed(k))) break;
                                 tc_fence_after();
-                                pv_product(w, w, v_pos(k), k == 0);
-                                mma_commit(&sh->pv_done[w]);
+                                pv_product(w, v_pos(k), k == 0);
                                 if (w == 1) free_stage(v_pos(k));
                                 if (k + 1 < nt) {
-                                    // overwrites P(k), which the product just issued reads:
-                                    // the tensor core takes them in this order
                                     if (w == 0 && !take(k_pos(k + 1), k_fixed(k + 1))) break;
                                     s_product(w, w, k_pos(k + 1));
-                                    mma_commit(&sh->s_full[w]);
                                     if (w == 1) free_stage(k_pos(k + 1));
                                 } else {
                                     mma_commit(&sh->q_empty[w]);
                                 }
                             }
                         }
-                        n2 += nt;
-                        ++pieces[0];
-                        ++pieces[1];
                     } else {
                         const int qs = ones++ & 1;
                         if (!wait(&sh->q_full[qs], q_use[qs]++)) break;
                         auto s_next = [&](int k) {
-                            if (!take(k_pos(k), k_fixed(k))) return;
+                            if (k >= nt || !take(k_pos(k), k_fixed(k))) return;
                             s_product(k & 1, qs, k_pos(k));
-                            mma_commit(&sh->s1_full[k & 1]);
                             free_stage(k_pos(k));
                         };
                         s_next(0);
+                        s_next(1);
+#pragma unroll 1
                         for (int k = 0; ok && k < nt; ++k) {
-                            if (k + 1 < nt) {
-                                s_next(k + 1);  // overwrites P(k - 1): its product went first
-                            } else {
-                                mma_commit(&sh->q_empty[qs]);
-                            }
-                            if (!wait(&sh->p1_full[k & 1], n1[k & 1]++)) break;
-                            if (k == 0 && !wait(&sh->o_free[0], pieces[0] + 1)) break;
+                            const int w = k & 1;
+                            if (!wait(&sh->p_full[w], p_use[w]++)) break;
+                            if (k == 0 && (!wait(&sh->o_free[0], n + 1) || !wait(&sh->o_free[1], n + 1))) break;
                             if (!take(v_pos(k), v_fixed(k))) break;
-                            tc_fence_after();
-                            pv_product(0, k & 1, v_pos(k), k == 0);
-                            mma_commit(&sh->pv_done[0]);
+                            pv_product(w, v_pos(k), k < 2);
                             free_stage(v_pos(k));
+                            s_next(k + 2);
                         }
-                        ++pieces[0];
                     }
                     rc += 2 * nt;
                 }
@@ -506,8 +511,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             }
         } else if (warp == 9) {
             // ------------------------------------------------ TMA producer
+            // walks the CTA's range (order: request, KV head, item), publishes
+            // its pieces to the other roles and loads their tiles
             const uint64_t pol = policy_evict_normal(), pol_first = policy_evict_first();
-            uint32_t pos = 0, q_use[2] = {0, 0}, ones = 0;
+            uint32_t pos = 0, n = 0, q_use[2] = {0, 0}, ones = 0;
             const int nb = kKeys / a.box;  // boxes per 64-d half of a cached tile
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t par) {
@@ -518,55 +525,122 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 return ok;
             };
-            for (bool has = wk.settle(); ok && has; has = wk.next()) {
-                const Piece& p = wk.p;
-                const int q0 = p.two ? 0 : ones++ & 1, q1 = p.two ? 1 : q0;
-                for (int s = q0; s <= q1; ++s) {
-                    if (!wait(&sh->q_empty[s], q_use[s] + 1)) break;
-                    ++q_use[s];
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&sh->q_full[s], (uint32_t)(a.tpq * a.grp * 128 * NH));
-                        for (int h = 0; h < NH; ++h)
-                            tma_load_4d(sQ + s * Shape::kTile + h * kHalfBytes, &tm_q, &sh->q_full[s], 64 * h,
-                                        p.g * a.grp, p.r.start + p.i0 + (s - q0) * a.tpq, 0, pol_first);
-                    }
+            auto publish = [&](const Piece& p) {
+                // the roles that might lag are done with the record's old piece
+                if (n >= kPieces) {
+                    ok = until(&sh->fixed, n - kPieces + 1) && pieces_done(n - kPieces + 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) return;
                 }
-                // keys that only this item reads need not stay in L2
-                const uint64_t pol_kv = p.r.items == 1 ? pol_first : pol;
-                for (int t = p.t0; ok && t < p.t1; ++t) {
-                    for (int v = 0; v < 2; ++v, ++pos) {
-                        const uint32_t s = pos % NST;
-                        if (!wait(&sh->empty[s], pos / NST + 1)) break;
-                        unsigned char* dst = ring + s * Shape::kTile;
+                if (lane == 0) {
+                    sh->pieces[n % kPieces] = p;
+                    __threadfence_block();
+                    *(volatile uint32_t*)&sh->published = n + 1;
+                }
+                __syncwarp();
+                ++n;
+            };
+            int b = bad ? a.B : sh->b, g = sh->g, q = sh->q, rel = sh->rel;  // rel: the item's start less my0
+            const int len = sh->len;
+            Request r = {};
+            if (b < a.B) r = request_of(a, a.q_start[b], a.q_start[b + 1], a.kv_len[b]);
+            Piece p = {};
+            while (ok && b < a.B && rel < len) {
+                const Item it = item_of(a, r, q);
+                p.t0 = rel >= 0 ? 0 : (it.two ? (-rel + kCost2 - 1) / kCost2 : (-rel + kCost1 - 1) / kCost1);
+                p.t1 = min(it.nt, it.two ? (len - rel + kCost2 - 1) / kCost2 : (len - rel + kCost1 - 1) / kCost1);
+                if (p.t0 < p.t1) {
+                    p.b = b;
+                    p.g = g;
+                    p.start = r.start;
+                    p.kv = r.kv;
+                    p.kvt = r.kvt;
+                    p.i0 = it.i0;
+                    p.i1 = it.i1;
+                    p.mode = it.two ? kTwo : it.i1 - it.i0 <= a.tps ? kQuad : kOne;
+                    p.slot = p.t0 > 0 ? 0 : p.t1 < it.nt ? 1 : -1;
+                    p.merged = r.merged;
+                    publish(p);
+                    if (!ok) break;
+                    const int q0 = it.two ? 0 : ones++ & 1, q1 = it.two ? 1 : q0;
+                    for (int s = q0; s <= q1; ++s) {
+                        if (!wait(&sh->q_empty[s], q_use[s] + 1)) break;
+                        ++q_use[s];
                         if (lane == 0) {
-                            mbar_arrive_expect_tx(&sh->full[s], Shape::kTile);
-                            *(volatile uint32_t*)&sh->issued = pos + 1;
-                        }
-                        __syncwarp();
-                        if (t >= p.r.kvt) {
-                            if (lane < NH)
-                                tma_load_4d(dst + lane * kHalfBytes, v ? &tm_vn : &tm_kn, &sh->full[s], 64 * lane,
-                                            p.g, p.r.start + (t - p.r.kvt) * kKeys, 0, pol);
-                            continue;
-                        }
-                        // one box per lane and step: `box` consecutive tokens of a page
-                        for (int x = lane; x < nb * NH; x += 32) {
-                            const int h = x / nb, row = (x - h * nb) * a.box;
-                            const int key = t * kKeys + row;
-                            int page = -1;  // a page past the cached keys, or a bad one, reads as zeros
-                            if (key < p.r.kv) {
-                                page = __ldg(a.page_table + (size_t)p.b * a.max_pages + key / a.P);
-                                if (page < 0 || page >= a.num_pages) {
-                                    raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
-                                    page = -1;
-                                }
+                            unsigned char* dst = sQ + s * Shape::kTile;
+                            const int row0 = r.start + it.i0 + (s - q0) * a.tpq;
+                            if (p.mode == kQuad) {
+                                mbar_arrive_expect_tx(&sh->q_full[s], (uint32_t)(4 * a.tps * a.grp * 128 * NH));
+                                for (int x = 0; x < 4 * NH; ++x)
+                                    tma_load_4d(dst + (x >> 2) * kHalfBytes + (x & 3) * 32 * 128, &tm_qs,
+                                                &sh->q_full[s], 64 * (x >> 2), g * a.grp, row0, 0, pol);
+                            } else {
+                                mbar_arrive_expect_tx(&sh->q_full[s], (uint32_t)(a.tpq * a.grp * 128 * NH));
+                                for (int h = 0; h < NH; ++h)
+                                    tma_load_4d(dst + h * kHalfBytes, &tm_q, &sh->q_full[s], 64 * h, g * a.grp, row0,
+                                                0, pol_first);
                             }
-                            tma_load_4d(dst + h * kHalfBytes + row * 128, v ? &tm_v : &tm_k, &sh->full[s], 64 * h,
-                                        p.g, key % a.P, page, pol_kv);
                         }
                     }
+                    // keys that only this item reads need not stay in L2
+                    const uint64_t pol_kv = r.items == 1 ? pol_first : pol;
+                    const int32_t* table = a.page_table + (size_t)b * a.max_pages;
+                    for (int t = p.t0; ok && t < p.t1; ++t) {
+                        for (int v = 0; v < 2; ++v, ++pos) {
+                            const uint32_t s = pos % NST;
+                            if (!wait(&sh->empty[s], pos / NST + 1)) break;
+                            unsigned char* dst = ring + s * Shape::kTile;
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(&sh->full[s], Shape::kTile);
+                                *(volatile uint32_t*)&sh->issued = pos + 1;
+                            }
+                            __syncwarp();
+                            if (t >= r.kvt) {
+                                if (lane < NH)
+                                    tma_load_4d(dst + lane * kHalfBytes, v ? &tm_vn : &tm_kn, &sh->full[s], 64 * lane,
+                                                g, r.start + (t - r.kvt) * kKeys, 0, pol);
+                                continue;
+                            }
+                            // one box per lane and step: `box` consecutive tokens of a page
+                            for (int x = lane; x < nb * NH; x += 32) {
+                                const int h = x / nb, row = (x - h * nb) * a.box;
+                                const int key = t * kKeys + row;
+                                int page = -1;  // a page past the cached keys, or a bad one, reads as zeros
+                                if (key < r.kv) {
+                                    page = __ldg(table + key / a.P);
+                                    if (page < 0 || page >= a.num_pages) {
+                                        raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
+                                        page = -1;
+                                    }
+                                }
+                                tma_load_4d(dst + h * kHalfBytes + row * 128, v ? &tm_v : &tm_k, &sh->full[s], 64 * h,
+                                            g, key % a.P, page, pol_kv);
+                            }
+                        }
+                    }
+                    if (p.slot == 1 && lane == 0) {
+                        // CTAs that hold a part: this one to the owner of the item's last tile
+                        const long long most = sh->total / a.cost_max;
+                        const int G = (int)min((long long)gridDim.x, max(most, 1ll));
+                        const long long last_at = sh->my0 + rel + (long long)(it.nt - 1) * it.w;
+                        const int last = (int)(((last_at + 1) * G - 1) / sh->total);
+                        ChunkCut c = {last - (int)blockIdx.x + 1, g, it.i0, it.i1, r.start, {0, 0, 0}};
+                        a.cuts[blockIdx.x] = c;
+                    }
                 }
+                // the next item
+                rel += it.cost;
+                if (++q < r.items) continue;
+                q = 0;
+                if (++g < a.Hkv) continue;
+                g = 0;
+                do {
+                    if (++b >= a.B) break;
+                    r = request_of(a, a.q_start[b], a.q_start[b + 1], a.kv_len[b]);
+                } while (r.items == 0);
             }
+            p.t0 = p.t1 = 0;
+            if (ok) publish(p);
             // drain: every copy has landed before the CTA may exit
             if (lane == 0) {
                 for (uint32_t i = pos > NST ? pos - NST : 0; i < pos; ++i)
@@ -621,20 +695,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             // merged tile are put into their rows, and infinities and NaN in V
             // rows that only some of the item's rows see are taken out and noted
             // for the epilogue.
-            uint32_t rc = 0, expect = 0;
-            int piece = 0;
+            uint32_t rc = 0, n = 0;
             bool ok = true;
-            auto until = [&](auto&& ready) {
-                const uint64_t t_start = global_ns();
-                bool good = true;
-                for (uint32_t it = 1; !ready(); ++it) {
-                    __nanosleep(32);
-                    if ((it & 63) == 0 && (*abort_flag || global_ns() - t_start > kWaitNs)) {
-                        good = ready();
-                        break;
-                    }
-                }
-                if (!good) give_up();
+            auto all_ok = [&](bool good) {
                 ok = __all_sync(0xffffffffu, good);
                 return ok;
             };
@@ -642,18 +705,17 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             // positions, so it first waits until the producer is at this one: the
             // barrier's phase is then the tile's, and stays it until the fix.
             auto landed = [&](uint32_t pos) {
-                if (!until([&] { return *(volatile uint32_t*)&sh->issued > pos; })) return false;
+                if (!all_ok(until(&sh->issued, pos + 1))) return false;
                 const bool good = mbar_wait_bounded(&sh->full[pos % NST], (pos / NST) & 1, abort_flag, kWaitNs);
                 if (!good) give_up();
-                ok = __all_sync(0xffffffffu, good);
-                return ok;
+                return all_ok(good);
             };
             auto done = [&](uint32_t s) {
-                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                proxy_fence();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->fix[s]);
             };
-            constexpr int kChunks = D / 8;          // 16-byte chunks of a row
+            constexpr int kChunks = D / 8;           // 16-byte chunks of a row
             constexpr int kRowsStep = 32 / kChunks;  // rows the warp covers at once
             const int ch = lane % kChunks, r_in = lane / kChunks;
             auto cell = [&](uint32_t s, int row) {
@@ -675,83 +737,82 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             };
             // makes `bad_from` this piece's, once every earlier piece has read its own
             auto claim = [&]() {
-                if (sh->bad_piece == piece) return true;
-                if (!until([&] { return *(volatile uint32_t*)&sh->epilogues >= expect; })) return false;
+                if (sh->bad_piece == (int)n) return true;
+                if (!all_ok(pieces_done(n))) return false;
                 for (int i = lane; i < 3 * D; i += 32) (&sh->bad_from[0][0])[i] = 0x7fffffff;
                 __syncwarp();
-                if (lane == 0) *(volatile int*)&sh->bad_piece = piece;
+                if (lane == 0) *(volatile int*)&sh->bad_piece = (int)n;
                 __syncwarp();
                 return true;
             };
-            for (bool has = wk.settle(); ok && has; has = wk.next()) {
-                const Piece& p = wk.p;
-                for (int t = p.t0; ok && t < p.t1; ++t) {
-                    const uint32_t kp = rc + 2 * (t - p.t0), vp = kp + 1;
+            Piece p;
+            while (all_ok(piece_at(n, p))) {
+                // the cached tile with free rows, and the new tiles that some row does not see whole
+                if (p.kv % kKeys && p.t0 < p.kvt && p.t1 >= p.kvt) {
+                    const uint32_t kp = rc + 2 * (p.kvt - 1 - p.t0), vp = kp + 1;
                     const uint32_t ks = kp % NST, vs = vp % NST;
-                    if (t < p.r.kvt) {
-                        const int m = p.r.kv - t * kKeys;  // cached keys of the tile
-                        if (m >= kKeys) continue;
-                        const int fresh = p.r.merged ? p.r.n : 0;
-                        if (fresh) {
-                            if (!landed(kp)) break;
-                            for (int i = r_in; i < fresh; i += kRowsStep)
-                                *cell(ks, m + i) = __ldg(reinterpret_cast<const uint4*>(
-                                                             a.k_new + ((size_t)(p.r.start + i) * a.Hkv + p.g) * D) + ch);
-                            done(ks);
-                        }
-                        if (!landed(vp)) break;
-                        for (int i0 = 0; i0 < fresh; i0 += kRowsStep) {
-                            const int i = i0 + r_in;
-                            uint4 w = make_uint4(0, 0, 0, 0);
-                            if (i < fresh)
-                                w = __ldg(reinterpret_cast<const uint4*>(
-                                              a.v_new + ((size_t)(p.r.start + i) * a.Hkv + p.g) * D) + ch);
-                            // the first new token is visible to every row
-                            const bool odd = i > 0 && (odd_pair(w.x) || odd_pair(w.y) || odd_pair(w.z) || odd_pair(w.w));
-                            if (__any_sync(0xffffffffu, odd)) {
-                                if (!claim()) break;
-                                if (odd) w = note(w, i);
-                            }
-                            if (i < fresh) *cell(vs, m + i) = w;
-                        }
-                        if (!ok) break;
-                        for (int row = m + fresh + r_in; row < kKeys; row += kRowsStep) *cell(vs, row) = make_uint4(0, 0, 0, 0);
-                        done(vs);
-                    } else {
-                        const int base = (t - p.r.kvt) * kKeys;
-                        if (base + kKeys <= p.i0 + 1) continue;  // every row sees all of it
-                        if (!landed(vp)) break;
-                        const int rows = min(kKeys, p.i1 - base);
-                        for (int r0 = max(0, p.i0 + 1 - base); r0 < rows; r0 += kRowsStep) {
-                            const int row = r0 + r_in;
-                            uint4 w = make_uint4(0, 0, 0, 0);
-                            if (row < rows) w = *cell(vs, row);
-                            const bool odd = odd_pair(w.x) || odd_pair(w.y) || odd_pair(w.z) || odd_pair(w.w);
-                            if (__any_sync(0xffffffffu, odd)) {
-                                if (!claim()) break;
-                                if (odd) *cell(vs, row) = note(w, base + row);
-                            }
-                        }
-                        if (!ok) break;
-                        for (int row = rows + r_in; row < kKeys; row += kRowsStep) *cell(vs, row) = make_uint4(0, 0, 0, 0);
-                        done(vs);
+                    const int m = p.kv % kKeys;  // cached keys of the tile
+                    // the item's new tokens (a row of an item sees none past its last)
+                    const int fresh = p.merged ? p.i1 : 0;
+                    if (fresh) {
+                        if (!landed(kp)) break;
+                        for (int i = r_in; i < fresh; i += kRowsStep)
+                            *cell(ks, m + i) = __ldg(
+                                reinterpret_cast<const uint4*>(a.k_new + ((size_t)(p.start + i) * a.Hkv + p.g) * D) + ch);
+                        done(ks);
                     }
+                    if (!landed(vp)) break;
+                    for (int i0 = 0; i0 < fresh; i0 += kRowsStep) {
+                        const int i = i0 + r_in;
+                        uint4 w = make_uint4(0, 0, 0, 0);
+                        if (i < fresh)
+                            w = __ldg(reinterpret_cast<const uint4*>(
+                                          a.v_new + ((size_t)(p.start + i) * a.Hkv + p.g) * D) + ch);
+                        const bool odd = odd_pair(w.x) || odd_pair(w.y) || odd_pair(w.z) || odd_pair(w.w);
+                        if (__any_sync(0xffffffffu, odd)) {
+                            if (!claim()) break;
+                            if (odd) w = note(w, i);
+                        }
+                        if (i < fresh) *cell(vs, m + i) = w;
+                    }
+                    if (!ok) break;
+                    for (int row = m + fresh + r_in; row < kKeys; row += kRowsStep) *cell(vs, row) = make_uint4(0, 0, 0, 0);
+                    done(vs);
                 }
+                const int first = max(p.t0, p.kvt + p.i0 / kKeys);
+                for (int t = first; ok && t < p.t1; ++t) {
+                    const int base = (t - p.kvt) * kKeys;
+                    if (base + kKeys <= p.i0 + 1) continue;  // every row sees all of it
+                    const uint32_t vp = rc + 2 * (t - p.t0) + 1, vs = vp % NST;
+                    if (!landed(vp)) break;
+                    const int rows = min(kKeys, p.i1 - base);
+                    for (int r0 = max(0, p.i0 + 1 - base); r0 < rows; r0 += kRowsStep) {
+                        const int row = r0 + r_in;
+                        uint4 w = make_uint4(0, 0, 0, 0);
+                        if (row < rows) w = *cell(vs, row);
+                        const bool odd = odd_pair(w.x) || odd_pair(w.y) || odd_pair(w.z) || odd_pair(w.w);
+                        if (__any_sync(0xffffffffu, odd)) {
+                            if (!claim()) break;
+                            if (odd) *cell(vs, row) = note(w, base + row);
+                        }
+                    }
+                    if (!ok) break;
+                    for (int row = rows + r_in; row < kKeys; row += kRowsStep) *cell(vs, row) = make_uint4(0, 0, 0, 0);
+                    done(vs);
+                }
+                if (!ok) break;
                 rc += 2 * (p.t1 - p.t0);
-                expect += p.two ? 8 : 4;
-                ++piece;
+                ++n;
+                if (lane == 0) *(volatile uint32_t*)&sh->fixed = n;
             }
         }
     } else {
         setmaxnreg_inc<kRegsHigh>();
         // ---------------------------------------------------- softmax and epilogue
-        const int wg = warp >> 2, rr = (warp & 3) * 32 + lane;  // row tile; row in it
-        const int tok = wg * a.tpq + rr / a.grp, head = rr % a.grp;
-        const bool row_used = rr < a.tpq * a.grp;
-        const uint32_t tm_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tm_o = tm_lane + kTmemO + wg * D;
-        uint32_t n2 = 0, n1[2] = {0, 0}, pvs = 0;
-        int piece = 0;
+        const int wg = warp >> 2, wq = warp & 3;  // warpgroup; its warp, a quarter of the TMEM lanes
+        const uint32_t tm_lane = tmem + ((uint32_t)(wq * 32) << 16);
+        const uint32_t tm_s = tm_lane + wg * kKeys, tm_o = tm_lane + kTmemO;
+        uint32_t s_use = 0, pvs = 0, ones = 0, met = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t par) {
             const bool good = mbar_wait_bounded(bar, par & 1, abort_flag, kWaitNs);
@@ -759,169 +820,303 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             ok = __all_sync(0xffffffffu, good);
             return ok;
         };
-        // the piece's product k is done; every product is waited for before the
-        // next one's weights are handed over, so the barrier is never two
-        // phases away
-        auto pv_wait = [&](int k) {
-            if (!wait(&sh->pv_done[wg], pvs + k)) return false;
+        // barrier of the eight softmax warps (a bounded one, like every wait)
+        auto soft_sync = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->meet);
+            return wait(&sh->meet, met++);
+        };
+        // The latest product of this warpgroup is done.  Every product is waited
+        // for before the next one's weights are handed over, so the barrier is
+        // never two phases away.
+        auto pv_wait = [&]() {
+            if (!wait(&sh->pv_done[wg], pvs - 1)) return false;
             tc_fence_after();
             return true;
         };
-        for (bool has = wk.settle(); ok && has; has = wk.next(), ++piece) {
-            const Piece& p = wk.p;
-            const int slot = wk.slot();
-            if (slot == 1 && threadIdx.x == 0) {
-                // CTAs that hold a part: this one to the owner of the item's last tile
-                const long long total_ = total, most = total_ / a.cost_max;
-                const int G = (int)min((long long)gridDim.x, max(most, 1ll));
-                const long long last_at = p.us + (long long)(p.nt - 1) * (p.two ? kCost2 : kCost1);
-                const int last = (int)(((last_at + 1) * G - 1) / total_);
-                ChunkCut* c = a.cuts + blockIdx.x;
-                c->g = p.g;
-                c->i0 = p.i0;
-                c->i1 = p.i1;
-                c->start = p.r.start;
-                c->parts = last - (int)blockIdx.x + 1;
-            }
-            if (wg == 1 && !p.two) continue;
+        Piece p;
+        for (uint32_t n = 0; ok && __all_sync(0xffffffffu, piece_at(n, p)); ++n) {
+            const bool quad = p.mode == kQuad;
+            const int rr = quad ? lane : wq * 32 + lane;  // row in its tile
+            const int tok = (p.mode == kTwo ? wg * a.tpq : 0) + rr / a.grp;
             const int i = p.i0 + tok;  // this row's token
-            const bool live = row_used && i < p.i1;
+            const bool live = rr < (quad ? a.tps : a.tpq) * a.grp && i < p.i1;
+            const int step = p.mode == kTwo ? 1 : 2, t_first = p.t0 + (p.mode == kTwo ? 0 : wg);
             float m_ref = -INFINITY, l = 0.f;
-            const int nt = p.t1 - p.t0;
-            for (int k = 0; k < nt; ++k) {
-                const int t = p.t0 + k;
-                const int buf = p.two ? wg : k & 1;
-                if (p.two) {
-                    if (!wait(&sh->s_full[wg], n2)) break;
-                    ++n2;
-                } else {
-                    if (!wait(&sh->s1_full[buf], n1[buf])) break;
-                    ++n1[buf];
-                }
-                tc_fence_after();
-                float s[kKeys];
-                {
-                    uint32_t (&u)[kKeys] = reinterpret_cast<uint32_t(&)[kKeys]>(s);
+            // the row's maximum has grown to top: l, and O if it holds products, follow
+            auto move_ref = [&](float top, bool has_o) {
+                const bool move = top > m_ref + 8.f;
+                const float m_new = move ? top : m_ref;
+                const float f = move ? ex2(m_ref - m_new) : 1.f;
+                if (has_o) {
+                    if (!pv_wait()) return;
+#pragma unroll 1
+                    for (int j = 0; j < D; j += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(tm_o + wg * D + j, o);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < kKeys; j += 32)
-                        tmem_ld_32x32b_x32(tm_lane + buf * kKeys + j, reinterpret_cast<uint32_t(&)[32]>(u[j]));
-                    tmem_ld_wait();
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st16(tm_o + wg * D + j, o);
+                    }
+                    tmem_st_wait();
                 }
-                // keys of this tile that the row sees
-                int seen;
-                if (t < p.r.kvt) {
-                    seen = p.r.kv - t * kKeys;
-                    if (p.r.merged && seen <= kKeys) seen += i + 1;
-                } else {
-                    seen = i + 1 - (t - p.r.kvt) * kKeys;
-                }
-                if (!live) seen = 0;
-                if (__any_sync(0xffffffffu, seen < kKeys)) {
+                l *= f;
+                m_ref = m_new;
+            };
+            // 32 scores, those from `seen` on hidden
+            auto scores = [&](int col, int seen, float (&s)[32]) {
+                tmem_ld_32x32b_x32(tm_s + col, reinterpret_cast<uint32_t(&)[32]>(s));
+                tmem_ld_wait();
+                if (__any_sync(0xffffffffu, seen < 32)) {
 #pragma unroll
-                    for (int j = 0; j < kKeys; ++j)
+                    for (int j = 0; j < 32; ++j)
                         if (j >= seen) s[j] = -INFINITY;
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            };
+            auto top_of = [&](const float (&s)[32], float top) {
+                float x = s[0], y = s[1];
 #pragma unroll
-                for (int j = 0; j < kKeys; j += 4)
+                for (int j = 2; j < 32; j += 4) {
+                    x = fmaxf(x, fmaxf(s[j], s[j + 1]));
+                    if (j + 2 < 32) y = fmaxf(y, fmaxf(s[j + 2], s[j + 3]));
+                }
+                return fmaxf(top, fmaxf(x, y));
+            };
+            // weights of 32 scores: rounded to bf16 for the product with V, summed in 32 bits
+            auto weights = [&](const float (&s)[32], float mu, unsigned long long& sum, uint32_t* w) {
+                const unsigned long long sc = pair(a.scale_log2, a.scale_log2), neg = pair(-mu, -mu);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[j + e]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-                const bool move = top > m_ref + 8.f;
-                if (__any_sync(0xffffffffu, move)) {
-                    const float m_new = move ? top : m_ref;
-                    const float f = move ? ex2(m_ref - m_new) : 1.f;
-                    if (k > 0) {
-                        if (!pv_wait(k - 1)) break;
+                for (int j = 0; j < 32; j += 2) {
+                    float x, y;
+                    unpair(fma2(pair(s[j], s[j + 1]), sc, neg), x, y);
+                    x = ex2(x);
+                    y = ex2(y);
+                    sum = add2(sum, pair(x, y));
+                    w[j >> 1] = pack_bf16(x, y);
+                }
+            };
+            for (int t = t_first; t < p.t1; t += step) {
+                if (!wait(&sh->s_full[wg], s_use++)) break;
+                tc_fence_after();
+                // keys of this tile that the row sees
+                int seen;
+                if (t < p.kvt) {
+                    seen = p.kv - t * kKeys;
+                    if (p.merged && seen <= kKeys) seen += i + 1;
+                } else {
+                    seen = i + 1 - (t - p.kvt) * kKeys;
+                }
+                if (!live) seen = 0;
+                const bool has_o = t != t_first;
+                if (quad) {
+                    // a quarter of the keys: the row's other quarters are other warps'
+                    float s[32];
+                    scores(wq * 32, seen - wq * 32, s);
+                    const float top = top_of(s, -INFINITY) * a.scale_log2;
+                    if (__any_sync(0xffffffffu, top > m_ref + 8.f)) {
+                        move_ref(top, has_o);
+                        if (!ok) break;
+                    }
+                    unsigned long long sum = 0;
+                    uint32_t w[16];
+                    weights(s, m_ref == -INFINITY ? 0.f : m_ref, sum, w);
+                    const uint32_t zero[16] = {};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (c != wq) tmem_st16(tm_s + c * 16, zero);
+                    tmem_st16(tm_s + wq * 16, w);
+                    float x, y;
+                    unpair(sum, x, y);
+                    l += x + y;
+                } else {
+                    if (!has_o) {
+                        float top = -INFINITY;
 #pragma unroll 1
-                        for (int j = 0; j < D; j += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(tm_o + j, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st16(tm_o + j, o);
+                        for (int c = 0; c < kKeys; c += 32) {
+                            float s[32];
+                            scores(c, seen - c, s);
+                            top = top_of(s, top);
                         }
-                        tmem_st_wait();
+                        move_ref(top * a.scale_log2, false);
                     }
-                    l *= f;
-                    m_ref = m_new;
-                }
-                const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                // weights are rounded to bf16 for the product with V; the sum
-                // takes them in 32 bits
+                    uint32_t w[kKeys / 2];
+                    unsigned long long sum;
+                    for (;;) {
+                        // weights by the reference as it is; done over in the rare
+                        // case that a maximum has outgrown it (S is still there)
+                        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+                        float top = -INFINITY;
+                        sum = 0;
 #pragma unroll
-                for (int j0 = 0; j0 < kKeys; j0 += 64) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int j = 0; j < 64; j += 2) {
-                        const float p0 = ex2(fmaf(s[j0 + j], a.scale_log2, -mu));
-                        const float p1 = ex2(fmaf(s[j0 + j + 1], a.scale_log2, -mu));
-                        sum[j & 2] += p0;
-                        sum[(j & 2) + 1] += p1;
-                        w[j >> 1] = pack_bf16(p0, p1);
+                        for (int c = 0; c < kKeys; c += 32) {
+                            float s[32];
+                            scores(c, seen - c, s);
+                            top = top_of(s, top);
+                            weights(s, mu, sum, w + c / 2);
+                        }
+                        top *= a.scale_log2;
+                        if (!__any_sync(0xffffffffu, top > m_ref + 8.f)) break;
+                        move_ref(top, has_o);
+                        if (!ok) break;
                     }
-                    tmem_st32(tm_lane + buf * kKeys + j0 / 2, w);
+                    if (!ok) break;
+                    tmem_st32(tm_s, w);
+                    tmem_st32(tm_s + 32, w + 32);
+                    float x, y;
+                    unpair(sum, x, y);
+                    l += x + y;
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tmem_st_wait();
-                if (k > 0 && !pv_wait(k - 1)) break;
+                if (has_o && !pv_wait()) break;
+                ++pvs;
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p.two ? &sh->p_full[wg] : &sh->p1_full[buf]);
+                if (lane == 0) mbar_arrive(&sh->p_full[wg]);
             }
             if (!ok) break;
             // ---- this piece's rows
-            if (!pv_wait(nt - 1)) break;
-            pvs += nt;
-            const bool odd = *(volatile int*)&sh->bad_piece == piece;
-            const float inv = 1.f / l;
-            __nv_bfloat16* orow = a.out + ((size_t)(p.r.start + i) * a.Hq + p.g * a.grp + head) * D;
-            float* part = a.part + ((size_t)blockIdx.x * 2 + max(slot, 0)) * (size_t)a.part_rows * (D + 2);
-            const int prow = wg * kTileRows + rr;
-            if (slot >= 0 && live) {
-                part[prow] = m_ref;
-                part[a.part_rows + prow] = l;
+            if (t_first < p.t1 && !pv_wait()) break;
+            if (p.mode != kTwo) {
+                // a warpgroup may have no tile of the piece: the other one's
+                // products are done too
+                tc_fence_before();
+                if (!soft_sync()) break;
+                tc_fence_after();
             }
-            float* po = part + 2 * a.part_rows + prow;
-#pragma unroll
-            for (int j = 0; j < D; j += 32) {
-                uint32_t o[32];
-                tmem_ld_32x32b_x32(tm_o + j, o);
-                tmem_ld_wait();
+            const bool odd = *(volatile int*)&sh->bad_piece == (int)n;
+            auto spoil = [&](float v, int d) {  // what the fixing warp took out, for the rows that see it
+                if (sh->bad_from[0][d] <= i) v += INFINITY;
+                if (sh->bad_from[1][d] <= i) v -= INFINITY;
+                if (sh->bad_from[2][d] <= i) v = NAN;
+                return v;
+            };
+            __nv_bfloat16* orow = a.out + ((size_t)(p.start + i) * a.Hq + p.g * a.grp + rr % a.grp) * D;
+            float* part = a.part + ((size_t)blockIdx.x * 2 + max(p.slot, 0)) * (size_t)a.part_rows * (D + 2);
+            const int prow = (p.mode == kTwo ? wg * kTileRows : 0) + rr;
+            // 8 dimensions of a finished row, or of its part
+            auto store8 = [&](float (&v)[8], int d, float inv) {
                 if (odd) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float v = __uint_as_float(o[e]);
-                        if (sh->bad_from[0][j + e] <= i) v += INFINITY;
-                        if (sh->bad_from[1][j + e] <= i) v -= INFINITY;
-                        if (sh->bad_from[2][j + e] <= i) v = NAN;
-                        o[e] = __float_as_uint(v);
-                    }
+                    for (int e = 0; e < 8; ++e) v[e] = spoil(v[e], d + e);
                 }
-                if (!live) continue;
-                if (slot >= 0) {
+                if (!live) return;
+                if (p.slot >= 0) {
+                    float* po = part + (size_t)(2 + d) * a.part_rows + prow;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) po[(size_t)(j + e) * a.part_rows] = __uint_as_float(o[e]);
+                    for (int e = 0; e < 8; ++e) po[(size_t)e * a.part_rows] = v[e];
                 } else {
+                    *reinterpret_cast<uint4*>(orow + d) =
+                        make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
+                                   pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
+                }
+            };
+            if (p.mode == kTwo) {
+                if (p.slot >= 0 && live) {
+                    part[prow] = m_ref;
+                    part[a.part_rows + prow] = l;
+                }
+                const float inv = 1.f / l;
+#pragma unroll 1
+                for (int d = 0; d < D; d += 32) {
+                    float o[32];
+                    tmem_ld_32x32b_x32(tm_o + wg * D + d, reinterpret_cast<uint32_t(&)[32]>(o));
+                    tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
-                        uint4 w;
-                        w.x = pack_bf16(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                        w.y = pack_bf16(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                        w.z = pack_bf16(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                        w.w = pack_bf16(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                        *reinterpret_cast<uint4*>(orow + j + e) = w;
+                        float v[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) v[x] = o[e + x];
+                        store8(v, d + e, inv);
                     }
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_n(&sh->o_free[wg], 2);
+            } else {
+                // both warpgroups hold a part of the rows (and, of 32 rows, every
+                // warp): they meet in the item's Q tile, whose products are done
+                const int qs = ones++ & 1;
+                float* meet = reinterpret_cast<float*>(sQ + qs * Shape::kTile);
+                // maxima and sums: [8][32] each, by warp, of its 32 rows
+                meet[warp * 32 + lane] = m_ref;
+                meet[256 + warp * 32 + lane] = l;
+                if (!soft_sync()) break;
+                const int w0 = quad ? 0 : wq, ws = quad ? 1 : 4;  // the warps that share this thread's row
+                float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+                for (int w = w0; w < 8; w += ws) top = fmaxf(top, meet[w * 32 + lane]);
+                const float mu = top == -INFINITY ? 0.f : top;
+#pragma unroll 1
+                for (int w = w0; w < 8; w += ws) sum += meet[256 + w * 32 + lane] * ex2(meet[w * 32 + lane] - mu);
+                const float inv = 1.f / sum;
+                const float f0 = ex2(meet[wq * 32 + lane] - mu), f1 = ex2(meet[(4 + wq) * 32 + lane] - mu);
+                if (p.slot >= 0 && live && wg == 0 && (!quad || wq == 0)) {
+                    part[prow] = top;
+                    part[a.part_rows + prow] = sum;
+                }
+                // 8 dimensions of both warpgroups' O; a part of no weight counts for
+                // nothing, whatever it holds
+                auto both8 = [&](int d, float (&v)[8]) {
+                    uint32_t x[8], y[8];
+                    tmem_ld8(tm_o + d, x);
+                    tmem_ld8(tm_o + D + d, y);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = (f0 > 0.f ? __uint_as_float(x[e]) * f0 : 0.f) +
+                               (f1 > 0.f ? __uint_as_float(y[e]) * f1 : 0.f);
+                };
+                if (!quad) {
+#pragma unroll 2
+                    for (int d = wg * (D / 2); d < (wg + 1) * (D / 2); d += 8) {
+                        float v[8];
+                        both8(d, v);
+                        store8(v, d, inv);
+                    }
+                } else {
+                    // the four quarters through shared memory, `width` dimensions at
+                    // a time: [4][rows][width + 1]
+                    float* stage = meet + 512;
+                    const int rows = (p.i1 - p.i0) * a.grp;
+                    const int width = rows <= 8 ? D : D / 4;
+#pragma unroll 1
+                    for (int d0 = 0; d0 < D; d0 += width) {
+                        for (int d = wg * (width / 2); d < (wg + 1) * (width / 2); d += 8) {
+                            float v[8];
+                            both8(d0 + d, v);
+                            if (live) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) stage[(wq * rows + lane) * (width + 1) + d + e] = v[e];
+                            }
+                        }
+                        if (!soft_sync()) break;
+                        // a row per thread again, 8 dimensions each: warps take slices
+                        if (live) {
+                            for (int d = warp * 8; d < width; d += 64) {
+                                float v[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const float* x = stage + lane * (width + 1) + d + e;
+                                    const int q1 = rows * (width + 1);
+                                    v[e] = (x[0] + x[q1]) + (x[2 * q1] + x[3 * q1]);
+                                }
+                                store8(v, d0 + d, inv);
+                            }
+                        }
+                        if (!soft_sync()) break;
+                    }
+                }
+                tc_fence_before();
+                proxy_fence();
+                if (!ok || !soft_sync()) break;
+                if (threadIdx.x == 0) mbar_arrive(&sh->q_empty[qs]);
+                if (lane == 0) {
+                    mbar_arrive(&sh->o_free[0]);
+                    mbar_arrive(&sh->o_free[1]);
+                }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sh->o_free[wg]);
-                atomicAdd(&sh->epilogues, 1u);
-            }
+            if (lane == 0) atomicAdd(&sh->epilogues[wg], 1u);
         }
     }
     tc_fence_before();
@@ -968,7 +1163,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
                 const float f0 = ex2(m - mu), f1 = ex2(mk - mu);
                 l = l * f0 + lk * f1;
 #pragma unroll
-                for (int e = 0; e < kJoinDims; ++e) o[e] = o[e] * f0 + ok[e] * f1;
+                for (int e = 0; e < kJoinDims; ++e)  // a part of no weight counts for nothing
+                    o[e] = (f0 > 0.f ? o[e] * f0 : 0.f) + (f1 > 0.f ? ok[e] * f1 : 0.f);
                 m = mn;
             }
         }
@@ -986,6 +1182,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
         for (int w = 0; w < used; ++w) {
             const float f = ex2(red[w][0][lane] - top);
             sum += f * red[w][1][lane];
+            if (f == 0.f) continue;
             x += f * red[w][2 + 2 * warp][lane];
             y += f * red[w][3 + 2 * warp][lane];
         }
@@ -1031,8 +1228,9 @@ cudaError_t launch_chunk_d(const ChunkArgs& a, const uint16_t* q, cudaStream_t s
         if (e != cudaSuccess) return e;
         configured |= 1ull << dev;
     }
-    CUtensorMap tq, tk, tv, tkn, tvn;
+    CUtensorMap tq, tqs, tk, tv, tkn, tvn;
     if (!encode_tiles(&tq, q, D, a.Hq, a.T, 1, a.grp, a.tpq) ||
+        !encode_tiles(&tqs, q, D, a.Hq, a.T, 1, a.grp, a.tps > 0 ? a.tps : a.tpq) ||
         !encode_tiles(&tk, a.k_pool, D, a.Hkv, a.P, a.num_pages, 1, a.box) ||
         !encode_tiles(&tv, a.v_pool, D, a.Hkv, a.P, a.num_pages, 1, a.box) ||
         !encode_tiles(&tkn, a.k_new, D, a.Hkv, a.T, 1, 1, kKeys) ||
@@ -1041,8 +1239,8 @@ cudaError_t launch_chunk_d(const ChunkArgs& a, const uint16_t* q, cudaStream_t s
         return cudaErrorInvalidValue;
     }
     const int grid = persistent_grid();
-    e = launch_kernel(false, chunk_kernel<D>, dim3(grid), dim3(kChunkThreads), ChunkShape<D>::kSmem(), st, tq, tk, tv,
-                      tkn, tvn, a);
+    e = launch_kernel(false, chunk_kernel<D>, dim3(grid), dim3(kChunkThreads), ChunkShape<D>::kSmem(), st, tq, tqs, tk,
+                      tv, tkn, tvn, a);
     if (e != cudaSuccess) return e;
     // about 8 blocks per CTA of the cut, whatever the rows
     const int groups = a.part_rows / 32, slices = groups >= 8 ? 1 : groups >= 4 ? 2 : groups >= 2 ? 4 : D / kJoinDims;
@@ -1063,6 +1261,7 @@ cudaError_t launch_chunk_attention(const isd_dims* d, int T, const uint16_t* q, 
     a.Hkv = d->Hkv;
     a.grp = d->Hq / d->Hkv;
     a.tpq = kTileRows / a.grp;
+    a.tps = 32 / a.grp;
     a.P = d->page_size;
     a.box = kKeys;  // the largest power of two up to a tile that divides the page
     while (d->page_size % a.box) a.box >>= 1;
