@@ -48,6 +48,11 @@ namespace {
 constexpr int kKeys = 128;              // keys per tile
 constexpr int kTileRows = 128;          // rows per tile
 constexpr int kHalfBytes = kKeys * 128; // 64 dimensions of a K, V or Q tile
+// A tile in shared memory is [64-d half][row][128 swizzled bytes].  A cached
+// tile whose pages are whole groups of 8 rows is [group][half][row of the
+// group][128 bytes] instead: then one box brings a page's rows with both halves
+// (a TMA copy takes the producer about 70 cycles to issue).
+constexpr int kGroupRows = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;
 // New tokens that are put into the free rows of the last cached tile instead
 // of a tile of their own.
@@ -69,6 +74,7 @@ struct ChunkCut {
 struct ChunkArgs {
     int B, T, Hq, Hkv, grp, P, box, num_pages, max_pages;
     int tpq, tps;   // tokens of a tile of 128 rows, and of one of 32
+    int grouped;    // layout of a cached tile (see kGroup)
     int cost_max;   // the dearest key tile that this T allows
     int part_rows;  // rows of a partial result
     float scale_log2;
@@ -118,6 +124,20 @@ struct Item {
     int nt, w, cost;  // key tiles, cost of one, of all
 };
 
+// Cost of a request's items of one KV head.
+ISD_DEVINL long long head_cost(const ChunkArgs& a, const Request& r) {
+    if (r.items == 0) return 0;
+    // all items but the last have two tiles; their new keys' tiles one by one
+    const int span = 2 * a.tpq, full = r.items - 1;
+    int fresh = 0;
+    if (!r.merged)
+        for (int q = 0, end = span; q < full; ++q, end += span) fresh += (end + kKeys - 1) / kKeys;
+    long long c = (long long)full * (kCost2 * (long long)r.kvt + kEnds2) + (long long)kCost2 * fresh;
+    const bool two = r.n - full * span > a.tpq;
+    const int nt = r.kvt + (r.merged ? 0 : (r.n + kKeys - 1) / kKeys);
+    return c + (two ? kCost2 * nt + kEnds2 : kCost1 * nt + kEnds1);
+}
+
 ISD_DEVINL Item item_of(const ChunkArgs& a, const Request& r, int q) {
     Item it;
     it.i0 = q * 2 * a.tpq;
@@ -158,7 +178,8 @@ struct ChunkShared {
     uint64_t meet, drain;
     Piece pieces[kPieces];
     long long my0, total;
-    int len, rel, b, g, q;
+    int len, rel, b, g, q;  // the range's length; its first item, which starts at `rel` in it
+    Request first;
     uint32_t tmem;
     int abort_flag, never;
     uint32_t published;  // pieces written by the producer
@@ -205,22 +226,66 @@ ISD_DEVINL void tmem_st32(uint32_t taddr, const uint32_t* r) {
         "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+ISD_DEVINL void tmem_ld32(uint32_t taddr, float (&r)[32]) {
+    sm100::tmem_ld_32x32b_x32(taddr, reinterpret_cast<uint32_t(&)[32]>(r));
+}
+// Waits for the loads so far; the values depend on it, so none is used before.
+ISD_DEVINL void tmem_arrived(float (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]),
+                   "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]),
+                   "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]));
+    asm volatile("" : "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31]));
+}
 ISD_DEVINL void tmem_ld8(uint32_t taddr, uint32_t* r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }
 
-// D(tmem) (+)= A(tmem) * B(smem desc), kind::f16
-ISD_DEVINL void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// The tensor-core instructions of the MMA warp: the whole warp runs its code and
+// one elected lane issues, so that descriptors stay in uniform registers (with a
+// branch for lane 0 around the code, an MMA took about 80 cycles to issue, 64
+// of the tensor core's).
+// (8-row groups 1024 bytes apart, or NH times that in a grouped tile).
+constexpr uint32_t kDescHi = 1u << 14 | 2u << 29;  // of smem_desc_sw128, less the groups' distance / 16
+ISD_DEVINL void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                       uint32_t accumulate) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred p, e;\n .reg .b64 da, db;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %6};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi | 1024u >> 4), "r"(b_hi)
+        : "memory");
+}
+ISD_DEVINL void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                       uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, e;\n .reg .b64 db;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+        " mov.b64 db, {%2, %5};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(b_hi)
+        : "memory");
+}
+ISD_DEVINL void commit_to(uint64_t* bar) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
         : "memory");
 }
 ISD_DEVINL void mbar_arrive_n(uint64_t* bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
+// box of whole 8-row groups of a page with all of a head's dimensions
+ISD_DEVINL void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int half, int group, int page,
+                            uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %3, %4, %5, %6}], [%2], %7;\n" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(0), "r"(half), "r"(group), "r"(page), "l"(policy)
+        : "memory");
 }
 
 ISD_DEVINL uint64_t policy_evict_normal() {
@@ -230,6 +295,18 @@ ISD_DEVINL uint64_t policy_evict_normal() {
 }
 
 ISD_DEVINL void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+
+// 32 bytes of a row: a whole sector in one store where the address allows
+ISD_DEVINL void store32(void* p, const uint32_t (&r)[8], bool aligned) {
+    if (aligned) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                     "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
+}
 
 // Whether one of two packed bf16 is infinite or NaN.
 ISD_DEVINL bool odd_pair(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
@@ -306,7 +383,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     bad = true;
                 } else {
                     r = request_of(a, s, e, kv);
-                    for (int q = 0; q < r.items; ++q) head += item_of(a, r, q).cost;
+                    head = head_cost(a, r);
                 }
             }
             const long long c = head * a.Hkv;
@@ -327,10 +404,19 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         };
         for (int b0 = 0; b0 < a.B; b0 += kChunkThreads) pass(b0 + (int)threadIdx.x);
         const long long total = run;
-        const long long most = total / a.cost_max;  // every CTA between an item's ends has a tile of it
+        const long long most = a.cost_max == kCost2 ? total / kCost2 : total / kCost1;  // every CTA between an item's ends has a tile of it
         const int G = (int)min((long long)gridDim.x, max(most, 1ll));
         const bool mine = (int)blockIdx.x < G;
-        const long long my0 = mine ? total * blockIdx.x / G : 0, my1 = mine ? total * (blockIdx.x + 1) / G : 0;
+        long long my0 = 0, my1 = 0;
+        if (mine) {
+            if (total < (1 << 23)) {  // the products fit in 32 bits
+                my0 = (unsigned)total * blockIdx.x / (unsigned)G;
+                my1 = (unsigned)total * (blockIdx.x + 1) / (unsigned)G;
+            } else {
+                my0 = total * blockIdx.x / G;
+                my1 = total * (blockIdx.x + 1) / G;
+            }
+        }
         if (threadIdx.x == 0) {
             sh->my0 = my0;
             sh->total = total;
@@ -339,14 +425,15 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         auto locate = [&](int b) {
             if (my0 >= my1 || my0 < before || my0 >= before + head * a.Hkv) return;
             long long rem = my0 - before;
-            const int g = (int)(rem / head);
-            rem -= g * head;
+            int g = 0;
+            for (; rem >= head; ++g) rem -= head;
             int q = 0;
             for (int w; (w = item_of(a, r, q).cost) <= rem; ++q) rem -= w;
             sh->b = b;
             sh->g = g;
             sh->q = q;
             sh->rel = -(int)rem;
+            sh->first = r;
         };
         if (a.B <= kChunkThreads) {
             locate(threadIdx.x);
@@ -397,116 +484,132 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         setmaxnreg_dec<kRegsLow>();
         if (warp == 8) {
             // ------------------------------------------------ MMA issuer
-            if (lane == 0) {
+            {
                 constexpr uint32_t idesc_s = idesc_bf16_f32(kTileRows, kKeys);
                 constexpr uint32_t idesc_o = idesc_bf16_f32(kTileRows, D) | (1u << 16);  // B = V: keys by rows
-                const uint64_t dq = smem_desc_sw128(smem_u32(sQ));
-                const uint64_t dk = smem_desc_sw128(smem_u32(ring));
-                // V as an operand with its dimensions contiguous: the two 64-d
-                // halves are kHalfBytes apart, 8-key groups 1024 bytes
-                const uint64_t dv = (dk & ~(0x3FFFull << 16)) | ((uint64_t)(kHalfBytes >> 4) << 16);
-                uint32_t rc = 0;     // ring position of the piece's first K tile
-                uint32_t fixes = 0;  // per stage: parity of the next fix
-                uint32_t q_use[2] = {0, 0}, p_use[2] = {0, 0}, ones = 0;
+                const uint32_t q_at = smem_u32(sQ) >> 4, ring_at = smem_u32(ring) >> 4;
+                struct Cursor {
+                    uint32_t st, ph;  // ring stage and parity of the next K (V) tile
+                } kc = {0, 0}, vc = {1, 0};
+                uint32_t fixes = 0;       // per stage: parity of the next fix
+                uint32_t q_ph = 0, p_ph = 0, ones = 0;  // parities: bit by Q slot, by warpgroup
                 bool ok = true;
                 auto wait = [&](uint64_t* bar, uint32_t par) {
-                    if (ok && !mbar_wait_bounded(bar, par & 1, abort_flag, kWaitNs)) {
-                        give_up();
-                        ok = false;
-                    }
+                    const bool good = mbar_wait_bounded(bar, par & 1, abort_flag, kWaitNs);
+                    if (!good) give_up();
+                    ok = __all_sync(0xffffffffu, good);
                     return ok;
                 };
-                auto take = [&](uint32_t pos, bool fixed) {  // the tile at ring position pos is there
-                    const uint32_t s = pos % NST;
-                    if (!wait(&sh->full[s], pos / NST)) return false;
+                auto wait_q = [&](int s) {
+                    const bool good = wait(&sh->q_full[s], q_ph >> s);
+                    q_ph ^= 1u << s;
+                    return good;
+                };
+                auto wait_p = [&](int w) {
+                    const bool good = wait(&sh->p_full[w], p_ph >> w);
+                    p_ph ^= 1u << w;
+                    tc_fence_after();
+                    return good;
+                };
+                // the next K (V) tile is there, and fixed: its stage
+                auto take = [&](Cursor& c, bool fixed, uint32_t& stage) {
+                    stage = c.st;
+                    if (!wait(&sh->full[c.st], c.ph)) return false;
                     if (fixed) {
-                        if (!wait(&sh->fix[s], fixes >> s)) return false;
-                        fixes ^= 1u << s;
+                        if (!wait(&sh->fix[c.st], fixes >> c.st)) return false;
+                        fixes ^= 1u << c.st;
+                    }
+                    c.st += 2;
+                    if (c.st >= NST) {
+                        c.st -= NST;
+                        c.ph ^= 1;
                     }
                     tc_fence_after();
                     return true;
                 };
-                auto free_stage = [&](uint32_t pos) { mma_commit(&sh->empty[pos % NST]); };
-                auto s_product = [&](int w, int qs, uint32_t pos) {
-                    const uint32_t k_off = (pos % NST) * Shape::kTile, q_off = (uint32_t)qs * Shape::kTile;
+                auto free_stage = [&](uint32_t stage) { commit_to(&sh->empty[stage]); };
+                // K: 8-row groups, 64-d halves; V, whose dimensions are contiguous,
+                // has the halves' distance as its leading offset and steps 16 keys
+                auto s_product = [&](int w, int qs, uint32_t stage, bool grouped) {
+                    const uint32_t k = ring_at + stage * (Shape::kTile >> 4) + (1u << 16);
+                    const uint32_t q = q_at + (uint32_t)qs * (Shape::kTile >> 4) + (1u << 16);
+                    const uint32_t half = (grouped ? 1024u : (uint32_t)kHalfBytes) >> 4;
+                    const uint32_t hi = kDescHi | (grouped ? 1024u * NH : 1024u) >> 4;
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t in = (uint32_t)((kk >> 2) * kHalfBytes + (kk & 3) * 32);
-                        mma_f16_ss(tmem + w * kKeys, dq + ((q_off + in) >> 4), dk + ((k_off + in) >> 4), idesc_s,
-                                   kk != 0);
-                    }
-                    mma_commit(&sh->s_full[w]);
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_ss(tmem + w * kKeys, q + (((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4),
+                               k + (kk >> 2) * half + (kk & 3) * 2, hi, idesc_s, kk != 0);
+                    commit_to(&sh->s_full[w]);
                 };
-                auto pv_product = [&](int w, uint32_t pos, bool first) {
-                    const uint32_t v_off = (pos % NST) * Shape::kTile;
+                auto pv_product = [&](int w, uint32_t stage, bool grouped, bool first) {
+                    const uint32_t half = (grouped ? 1024u : (uint32_t)kHalfBytes) >> 4;
+                    const uint32_t v = ring_at + stage * (Shape::kTile >> 4) + (half << 16);
+                    const uint32_t hi = kDescHi | (grouped ? 1024u * NH : 1024u) >> 4;
+                    const uint32_t step = (grouped ? 2048u * NH : 2048u) >> 4;
 #pragma unroll
                     for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_f16_ts(tmem + kTmemO + w * D, tmem + w * kKeys + kk * 8, dv + ((v_off + kk * 2048) >> 4),
-                                   idesc_o, !(first && kk == 0));
-                    mma_commit(&sh->pv_done[w]);
+                        mma_ts(tmem + kTmemO + w * D, tmem + w * kKeys + kk * 8, v + kk * step, hi, idesc_o,
+                               !(first && kk == 0));
+                    commit_to(&sh->pv_done[w]);
                 };
                 Piece p;
-                for (uint32_t n = 0; ok && piece_at(n, p); ++n) {
+                for (uint32_t n = 0; ok && __all_sync(0xffffffffu, piece_at(n, p)); ++n) {
                     const int nt = p.t1 - p.t0;
+                    const int kvk = p.kvt - p.t0;  // cached tiles ahead
+                    auto grouped = [&](int k) { return a.grouped && k < kvk; };
                     // which tiles the fixing warp touches first
-                    auto k_fixed = [&](int k) { return p.merged && p.t0 + k == p.kvt - 1; };
-                    auto v_fixed = [&](int k) {
-                        const int t = p.t0 + k;
-                        if (t < p.kvt) return (t + 1) * kKeys > p.kv;
-                        return (t + 1 - p.kvt) * kKeys > p.i0 + 1;
-                    };
-                    auto k_pos = [&](int k) { return rc + 2 * k; };
-                    auto v_pos = [&](int k) { return rc + 2 * k + 1; };
+                    const int k_fix = p.merged ? kvk - 1 : -1, v_fix = p.kv % kKeys ? kvk - 1 : -1;
+                    const int new_fix = kvk + (p.i0 + 1) / kKeys;
+                    auto v_fixed = [&](int k) { return k == v_fix || k >= new_fix; };
+                    uint32_t ks, vs;
                     // S(k + ...) overwrites P(k), which the product issued before it
                     // reads: the tensor core takes them in this order
                     if (p.mode == kTwo) {
-                        if (!wait(&sh->q_full[0], q_use[0]++) || !wait(&sh->q_full[1], q_use[1]++)) break;
-                        if (!take(k_pos(0), k_fixed(0))) break;
-                        s_product(0, 0, k_pos(0));
-                        s_product(1, 1, k_pos(0));
-                        free_stage(k_pos(0));
-                        for (int k = 0; ok && k < nt; ++k) {
+                        if (!wait_q(0) || !wait_q(1) || !take(kc, k_fix == 0, ks)) break;
+                        s_product(0, 0, ks, grouped(0));
+                        s_product(1, 1, ks, grouped(0));
+                        free_stage(ks);
+                        if (!wait(&sh->o_free[0], n + 1) || !wait(&sh->o_free[1], n + 1)) break;
 #pragma unroll 1
-                            for (int w = 0; w < 2; ++w) {
-                                if (!wait(&sh->p_full[w], p_use[w]++)) break;
-                                if (k == 0 && !wait(&sh->o_free[w], n + 1)) break;
-                                if (w == 0 && !take(v_pos(k), v_fixed(k))) break;
-                                tc_fence_after();
-                                pv_product(w, v_pos(k), k == 0);
-                                if (w == 1) free_stage(v_pos(k));
-                                if (k + 1 < nt) {
-                                    if (w == 0 && !take(k_pos(k + 1), k_fixed(k + 1))) break;
-                                    s_product(w, w, k_pos(k + 1));
-                                    if (w == 1) free_stage(k_pos(k + 1));
-                                } else {
-                                    mma_commit(&sh->q_empty[w]);
-                                }
+                        for (int k = 0; k < nt; ++k) {
+                            const bool more = k + 1 < nt;
+                            if (!take(vc, v_fixed(k), vs) || !wait_p(0)) break;
+                            pv_product(0, vs, grouped(k), k == 0);
+                            if (more) {
+                                if (!take(kc, k + 1 == k_fix, ks)) break;
+                                s_product(0, 0, ks, grouped(k + 1));
+                            }
+                            if (!wait_p(1)) break;
+                            pv_product(1, vs, grouped(k), k == 0);
+                            free_stage(vs);
+                            if (more) {
+                                s_product(1, 1, ks, grouped(k + 1));
+                                free_stage(ks);
                             }
                         }
+                        commit_to(&sh->q_empty[0]);
+                        commit_to(&sh->q_empty[1]);
                     } else {
                         const int qs = ones++ & 1;
-                        if (!wait(&sh->q_full[qs], q_use[qs]++)) break;
                         auto s_next = [&](int k) {
-                            if (k >= nt || !take(k_pos(k), k_fixed(k))) return;
-                            s_product(k & 1, qs, k_pos(k));
-                            free_stage(k_pos(k));
+                            if (k >= nt) return true;
+                            if (!take(kc, k == k_fix, ks)) return false;
+                            s_product(k & 1, qs, ks, grouped(k));
+                            free_stage(ks);
+                            return true;
                         };
-                        s_next(0);
-                        s_next(1);
+                        if (!wait_q(qs) || !s_next(0) || !s_next(1)) break;
+                        if (!wait(&sh->o_free[0], n + 1) || !wait(&sh->o_free[1], n + 1)) break;
 #pragma unroll 1
-                        for (int k = 0; ok && k < nt; ++k) {
-                            const int w = k & 1;
-                            if (!wait(&sh->p_full[w], p_use[w]++)) break;
-                            if (k == 0 && (!wait(&sh->o_free[0], n + 1) || !wait(&sh->o_free[1], n + 1))) break;
-                            if (!take(v_pos(k), v_fixed(k))) break;
-                            pv_product(w, v_pos(k), k < 2);
-                            free_stage(v_pos(k));
-                            s_next(k + 2);
+                        for (int k = 0; k < nt; ++k) {
+                            if (!take(vc, v_fixed(k), vs) || !wait_p(k & 1)) break;
+                            pv_product(k & 1, vs, grouped(k), k < 2);
+                            free_stage(vs);
+                            if (!s_next(k + 2)) break;
                         }
                     }
-                    rc += 2 * nt;
                 }
-                mma_commit(&sh->drain);
+                commit_to(&sh->drain);
                 mbar_wait_bounded(&sh->drain, 0, &sh->never, kWaitNs);
             }
         } else if (warp == 9) {
@@ -515,7 +618,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             // its pieces to the other roles and loads their tiles
             const uint64_t pol = policy_evict_normal(), pol_first = policy_evict_first();
             uint32_t pos = 0, n = 0, q_use[2] = {0, 0}, ones = 0;
-            const int nb = kKeys / a.box;  // boxes per 64-d half of a cached tile
+            const int nb = kKeys / a.box, boxes = a.grouped ? nb : nb * NH;  // boxes of a cached tile
+            const int x_half = lane / nb, x_row = (lane - x_half * nb) * a.box;
+            const bool one_each = boxes <= 32;  // else the boxes' pages are looked up as they go
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t par) {
                 if (lane == 0 && !mbar_wait_bounded(bar, par & 1, abort_flag, kWaitNs)) {
@@ -542,8 +647,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             };
             int b = bad ? a.B : sh->b, g = sh->g, q = sh->q, rel = sh->rel;  // rel: the item's start less my0
             const int len = sh->len;
-            Request r = {};
-            if (b < a.B) r = request_of(a, a.q_start[b], a.q_start[b + 1], a.kv_len[b]);
+            Request r = sh->first;
             Piece p = {};
             while (ok && b < a.B && rel < len) {
                 const Item it = item_of(a, r, q);
@@ -560,6 +664,26 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     p.mode = it.two ? kTwo : it.i1 - it.i0 <= a.tps ? kQuad : kOne;
                     p.slot = p.t0 > 0 ? 0 : p.t1 < it.nt ? 1 : -1;
                     p.merged = r.merged;
+                    // box x = lane + 32 j of a cached tile: rows from (x % nb) * box
+                    // on, of 64-d half x / nb (of both when grouped).  The pages of
+                    // the next tile are fetched while this one is loaded.
+                    const int32_t* table = a.page_table + (size_t)b * a.max_pages;
+                    auto page_of = [&](int key) {
+                        int page = -1;  // a page past the cached keys, or a bad one, reads as zeros
+                        if (key < r.kv) {
+                            page = __ldg(table + key / a.P);
+                            if (page < 0 || page >= a.num_pages) {
+                                raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
+                                page = -1;
+                            }
+                        }
+                        return page;
+                    };
+                    int next_page = -1, next_in = 0;
+                    if (one_each && p.t0 < r.kvt) {
+                        next_page = page_of(p.t0 * kKeys + x_row);
+                        next_in = (p.t0 * kKeys + x_row) % a.P;
+                    }
                     publish(p);
                     if (!ok) break;
                     const int q0 = it.two ? 0 : ones++ & 1, q1 = it.two ? 1 : q0;
@@ -584,8 +708,12 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     }
                     // keys that only this item reads need not stay in L2
                     const uint64_t pol_kv = r.items == 1 ? pol_first : pol;
-                    const int32_t* table = a.page_table + (size_t)b * a.max_pages;
                     for (int t = p.t0; ok && t < p.t1; ++t) {
+                        const int page = next_page, in = next_in;
+                        if (one_each && t + 1 < p.t1 && t + 1 < r.kvt) {
+                            next_page = page_of((t + 1) * kKeys + x_row);
+                            next_in = ((t + 1) * kKeys + x_row) % a.P;
+                        }
                         for (int v = 0; v < 2; ++v, ++pos) {
                             const uint32_t s = pos % NST;
                             if (!wait(&sh->empty[s], pos / NST + 1)) break;
@@ -599,22 +727,20 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                                 if (lane < NH)
                                     tma_load_4d(dst + lane * kHalfBytes, v ? &tm_vn : &tm_kn, &sh->full[s], 64 * lane,
                                                 g, r.start + (t - r.kvt) * kKeys, 0, pol);
-                                continue;
-                            }
-                            // one box per lane and step: `box` consecutive tokens of a page
-                            for (int x = lane; x < nb * NH; x += 32) {
-                                const int h = x / nb, row = (x - h * nb) * a.box;
-                                const int key = t * kKeys + row;
-                                int page = -1;  // a page past the cached keys, or a bad one, reads as zeros
-                                if (key < r.kv) {
-                                    page = __ldg(table + key / a.P);
-                                    if (page < 0 || page >= a.num_pages) {
-                                        raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
-                                        page = -1;
-                                    }
+                            } else if (a.grouped) {
+                                if (lane < nb)
+                                    tma_load_5d(dst + x_row * 128 * NH, v ? &tm_v : &tm_k, &sh->full[s], g * NH,
+                                                in / kGroupRows, page, pol_kv);
+                            } else if (one_each) {
+                                if (lane < boxes)
+                                    tma_load_4d(dst + x_half * kHalfBytes + x_row * 128, v ? &tm_v : &tm_k, &sh->full[s],
+                                                64 * x_half, g, in, page, pol_kv);
+                            } else {
+                                for (int x = lane; x < boxes; x += 32) {
+                                    const int h = x / nb, row = (x - h * nb) * a.box, key = t * kKeys + row;
+                                    tma_load_4d(dst + h * kHalfBytes + row * 128, v ? &tm_v : &tm_k, &sh->full[s],
+                                                64 * h, g, key % a.P, page_of(key), pol_kv);
                                 }
-                                tma_load_4d(dst + h * kHalfBytes + row * 128, v ? &tm_v : &tm_k, &sh->full[s], 64 * h,
-                                            g, key % a.P, page, pol_kv);
                             }
                         }
                     }
@@ -718,9 +844,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             constexpr int kChunks = D / 8;           // 16-byte chunks of a row
             constexpr int kRowsStep = 32 / kChunks;  // rows the warp covers at once
             const int ch = lane % kChunks, r_in = lane / kChunks;
-            auto cell = [&](uint32_t s, int row) {
-                return reinterpret_cast<uint4*>(ring + s * Shape::kTile + (ch >> 3) * kHalfBytes + row * 128 +
-                                                (((ch & 7) ^ (row & 7)) << 4));
+            auto cell = [&](uint32_t s, int row, bool grouped) {
+                const int at = grouped ? (row >> 3) * (1024 * NH) + (ch >> 3) * 1024 + (row & 7) * 128
+                                       : (ch >> 3) * kHalfBytes + row * 128;
+                return reinterpret_cast<uint4*>(ring + s * Shape::kTile + at + (((ch & 7) ^ (row & 7)) << 4));
             };
             // notes what is not finite in this lane's chunk of token `tok` and returns the chunk without it
             auto note = [&](uint4 w, int tok) {
@@ -757,7 +884,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     if (fresh) {
                         if (!landed(kp)) break;
                         for (int i = r_in; i < fresh; i += kRowsStep)
-                            *cell(ks, m + i) = __ldg(
+                            *cell(ks, m + i, a.grouped) = __ldg(
                                 reinterpret_cast<const uint4*>(a.k_new + ((size_t)(p.start + i) * a.Hkv + p.g) * D) + ch);
                         done(ks);
                     }
@@ -773,10 +900,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                             if (!claim()) break;
                             if (odd) w = note(w, i);
                         }
-                        if (i < fresh) *cell(vs, m + i) = w;
+                        if (i < fresh) *cell(vs, m + i, a.grouped) = w;
                     }
                     if (!ok) break;
-                    for (int row = m + fresh + r_in; row < kKeys; row += kRowsStep) *cell(vs, row) = make_uint4(0, 0, 0, 0);
+                    for (int row = m + fresh + r_in; row < kKeys; row += kRowsStep)
+                        *cell(vs, row, a.grouped) = make_uint4(0, 0, 0, 0);
                     done(vs);
                 }
                 const int first = max(p.t0, p.kvt + p.i0 / kKeys);
@@ -789,15 +917,16 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     for (int r0 = max(0, p.i0 + 1 - base); r0 < rows; r0 += kRowsStep) {
                         const int row = r0 + r_in;
                         uint4 w = make_uint4(0, 0, 0, 0);
-                        if (row < rows) w = *cell(vs, row);
+                        if (row < rows) w = *cell(vs, row, false);
                         const bool odd = odd_pair(w.x) || odd_pair(w.y) || odd_pair(w.z) || odd_pair(w.w);
                         if (__any_sync(0xffffffffu, odd)) {
                             if (!claim()) break;
-                            if (odd) *cell(vs, row) = note(w, base + row);
+                            if (odd) *cell(vs, row, false) = note(w, base + row);
                         }
                     }
                     if (!ok) break;
-                    for (int row = rows + r_in; row < kKeys; row += kRowsStep) *cell(vs, row) = make_uint4(0, 0, 0, 0);
+                    for (int row = rows + r_in; row < kKeys; row += kRowsStep)
+                        *cell(vs, row, false) = make_uint4(0, 0, 0, 0);
                     done(vs);
                 }
                 if (!ok) break;
@@ -843,11 +972,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const bool live = rr < (quad ? a.tps : a.tpq) * a.grp && i < p.i1;
             const int step = p.mode == kTwo ? 1 : 2, t_first = p.t0 + (p.mode == kTwo ? 0 : wg);
             float m_ref = -INFINITY, l = 0.f;
-            // the row's maximum has grown to top: l, and O if it holds products, follow
+            // the row's maximum is top: the reference, l, and O if it holds products, follow
             auto move_ref = [&](float top, bool has_o) {
-                const bool move = top > m_ref + 8.f;
-                const float m_new = move ? top : m_ref;
-                const float f = move ? ex2(m_ref - m_new) : 1.f;
+                const float m_new = fmaxf(m_ref, top);
+                const float f = m_new > m_ref ? ex2(m_ref - m_new) : 1.f;
                 if (has_o) {
                     if (!pv_wait()) return;
 #pragma unroll 1
@@ -864,24 +992,21 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 l *= f;
                 m_ref = m_new;
             };
-            // 32 scores, those from `seen` on hidden
-            auto scores = [&](int col, int seen, float (&s)[32]) {
-                tmem_ld_32x32b_x32(tm_s + col, reinterpret_cast<uint32_t(&)[32]>(s));
-                tmem_ld_wait();
+            auto hide = [&](float (&s)[32], int seen) {  // scores from `seen` on
                 if (__any_sync(0xffffffffu, seen < 32)) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (j >= seen) s[j] = -INFINITY;
                 }
             };
-            auto top_of = [&](const float (&s)[32], float top) {
-                float x = s[0], y = s[1];
+            auto top_of = [&](const float (&s)[32]) {
+                float x = fmaxf(s[0], s[1]), y = fmaxf(s[2], s[3]);
 #pragma unroll
-                for (int j = 2; j < 32; j += 4) {
+                for (int j = 4; j < 32; j += 4) {
                     x = fmaxf(x, fmaxf(s[j], s[j + 1]));
-                    if (j + 2 < 32) y = fmaxf(y, fmaxf(s[j + 2], s[j + 3]));
+                    y = fmaxf(y, fmaxf(s[j + 2], s[j + 3]));
                 }
-                return fmaxf(top, fmaxf(x, y));
+                return fmaxf(x, y);
             };
             // weights of 32 scores: rounded to bf16 for the product with V, summed in 32 bits
             auto weights = [&](const float (&s)[32], float mu, unsigned long long& sum, uint32_t* w) {
@@ -909,64 +1034,76 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 }
                 if (!live) seen = 0;
                 const bool has_o = t != t_first;
+                // Weights are taken by the reference as it is.  Only when a row's sum
+                // of them passes 2^10 (then one may be large) is its maximum looked
+                // up and the reference moved, and they are done over: S is still there.
+                float sum;
                 if (quad) {
                     // a quarter of the keys: the row's other quarters are other warps'
                     float s[32];
-                    scores(wq * 32, seen - wq * 32, s);
-                    const float top = top_of(s, -INFINITY) * a.scale_log2;
-                    if (__any_sync(0xffffffffu, top > m_ref + 8.f)) {
-                        move_ref(top, has_o);
+                    tmem_ld32(tm_s + wq * 32, s);
+                    tmem_arrived(s);
+                    hide(s, seen - wq * 32);
+                    if (!has_o) move_ref(top_of(s) * a.scale_log2, false);
+                    uint32_t w[16];
+                    for (;;) {
+                        unsigned long long acc = 0;
+                        weights(s, m_ref == -INFINITY ? 0.f : m_ref, acc, w);
+                        float y;
+                        unpair(acc, sum, y);
+                        sum += y;
+                        if (!__any_sync(0xffffffffu, sum > 1024.f)) break;
+                        move_ref(top_of(s) * a.scale_log2, has_o);
                         if (!ok) break;
                     }
-                    unsigned long long sum = 0;
-                    uint32_t w[16];
-                    weights(s, m_ref == -INFINITY ? 0.f : m_ref, sum, w);
+                    if (!ok) break;
                     const uint32_t zero[16] = {};
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         if (c != wq) tmem_st16(tm_s + c * 16, zero);
                     tmem_st16(tm_s + wq * 16, w);
-                    float x, y;
-                    unpair(sum, x, y);
-                    l += x + y;
                 } else {
-                    if (!has_o) {
-                        float top = -INFINITY;
-#pragma unroll 1
-                        for (int c = 0; c < kKeys; c += 32) {
-                            float s[32];
-                            scores(c, seen - c, s);
-                            top = top_of(s, top);
-                        }
-                        move_ref(top * a.scale_log2, false);
-                    }
+                    bool look = !has_o;
                     uint32_t w[kKeys / 2];
-                    unsigned long long sum;
                     for (;;) {
-                        // weights by the reference as it is; done over in the rare
-                        // case that a maximum has outgrown it (S is still there)
-                        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-                        float top = -INFINITY;
-                        sum = 0;
-#pragma unroll
-                        for (int c = 0; c < kKeys; c += 32) {
-                            float s[32];
-                            scores(c, seen - c, s);
-                            top = top_of(s, top);
-                            weights(s, mu, sum, w + c / 2);
+                        float s0[32], s1[32];
+                        if (look) {
+                            float top = -INFINITY;
+#pragma unroll 1
+                            for (int c = 0; c < kKeys; c += 32) {
+                                tmem_ld32(tm_s + c, s0);
+                                tmem_arrived(s0);
+                                hide(s0, seen - c);
+                                top = fmaxf(top, top_of(s0));
+                            }
+                            move_ref(top * a.scale_log2, has_o);
+                            if (!ok) break;
                         }
-                        top *= a.scale_log2;
-                        if (!__any_sync(0xffffffffu, top > m_ref + 8.f)) break;
-                        move_ref(top, has_o);
-                        if (!ok) break;
+                        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+                        unsigned long long acc = 0;
+                        tmem_ld32(tm_s, s0);
+#pragma unroll
+                        for (int c = 0; c < kKeys; c += 64) {
+                            tmem_arrived(s0);
+                            tmem_ld32(tm_s + c + 32, s1);
+                            hide(s0, seen - c);
+                            weights(s0, mu, acc, w + c / 2);
+                            tmem_arrived(s1);
+                            if (c + 64 < kKeys) tmem_ld32(tm_s + c + 64, s0);
+                            hide(s1, seen - c - 32);
+                            weights(s1, mu, acc, w + c / 2 + 16);
+                        }
+                        float y;
+                        unpair(acc, sum, y);
+                        sum += y;
+                        if (look || !__any_sync(0xffffffffu, sum > 1024.f)) break;
+                        look = true;
                     }
                     if (!ok) break;
                     tmem_st32(tm_s, w);
                     tmem_st32(tm_s + 32, w + 32);
-                    float x, y;
-                    unpair(sum, x, y);
-                    l += x + y;
                 }
+                l += sum;
                 tmem_st_wait();
                 if (has_o && !pv_wait()) break;
                 ++pvs;
@@ -1017,17 +1154,34 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     part[a.part_rows + prow] = l;
                 }
                 const float inv = 1.f / l;
+                const bool wide = ((uintptr_t)a.out & 31) == 0;
 #pragma unroll 1
                 for (int d = 0; d < D; d += 32) {
                     float o[32];
-                    tmem_ld_32x32b_x32(tm_o + wg * D + d, reinterpret_cast<uint32_t(&)[32]>(o));
-                    tmem_ld_wait();
+                    tmem_ld32(tm_o + wg * D + d, o);
+                    tmem_arrived(o);
+                    if (odd) {
+#pragma unroll 1
+                        for (int e = 0; e < 32; ++e) {
+                            const float v = spoil(0.f, d + e);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        float v[8];
+                            for (int x = 0; x < 32; ++x)
+                                if (x == e) o[x] += v;
+                        }
+                    }
+                    if (!live) continue;
+                    if (p.slot >= 0) {
+                        float* po = part + (size_t)(2 + d) * a.part_rows + prow;
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) v[x] = o[e + x];
-                        store8(v, d + e, inv);
+                        for (int e = 0; e < 32; ++e) po[(size_t)e * a.part_rows] = o[e];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 16) {
+                            uint32_t h[8];
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) h[x] = pack_bf16(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv);
+                            store32(orow + d + e, h, wide);
+                        }
                     }
                 }
                 tc_fence_before();
@@ -1206,6 +1360,20 @@ bool encode_tiles(CUtensorMap* m, const void* ptr, uint64_t D, uint64_t heads, u
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// pages of whole 8-row groups: see kGroupRows
+bool encode_groups(CUtensorMap* m, const void* ptr, uint64_t D, const ChunkArgs& a) {
+    EncodeTiledFn fn = get_encode_fn();
+    if (!fn) return false;
+    const uint64_t row = (uint64_t)a.Hkv * D * 2;
+    const cuuint64_t gd[5] = {64, kGroupRows, a.Hkv * D / 64, (uint64_t)a.P / kGroupRows, (uint64_t)a.num_pages};
+    const cuuint64_t gs[4] = {row, 128, kGroupRows * row, a.P * row};
+    const cuuint32_t bx[5] = {64, kGroupRows, (uint32_t)D / 64, (uint32_t)a.box / kGroupRows, 1};
+    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), gd, gs, bx, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D>
 cudaError_t launch_chunk_d(const ChunkArgs& a, const uint16_t* q, cudaStream_t st) {
     static unsigned long long configured = 0;  // bit per device
@@ -1231,8 +1399,8 @@ cudaError_t launch_chunk_d(const ChunkArgs& a, const uint16_t* q, cudaStream_t s
     CUtensorMap tq, tqs, tk, tv, tkn, tvn;
     if (!encode_tiles(&tq, q, D, a.Hq, a.T, 1, a.grp, a.tpq) ||
         !encode_tiles(&tqs, q, D, a.Hq, a.T, 1, a.grp, a.tps > 0 ? a.tps : a.tpq) ||
-        !encode_tiles(&tk, a.k_pool, D, a.Hkv, a.P, a.num_pages, 1, a.box) ||
-        !encode_tiles(&tv, a.v_pool, D, a.Hkv, a.P, a.num_pages, 1, a.box) ||
+        !(a.grouped ? encode_groups(&tk, a.k_pool, D, a) : encode_tiles(&tk, a.k_pool, D, a.Hkv, a.P, a.num_pages, 1, a.box)) ||
+        !(a.grouped ? encode_groups(&tv, a.v_pool, D, a) : encode_tiles(&tv, a.v_pool, D, a.Hkv, a.P, a.num_pages, 1, a.box)) ||
         !encode_tiles(&tkn, a.k_new, D, a.Hkv, a.T, 1, 1, kKeys) ||
         !encode_tiles(&tvn, a.v_new, D, a.Hkv, a.T, 1, 1, kKeys)) {
         set_error_detail("chunk attention: tensor map");
@@ -1265,6 +1433,7 @@ cudaError_t launch_chunk_attention(const isd_dims* d, int T, const uint16_t* q, 
     a.P = d->page_size;
     a.box = kKeys;  // the largest power of two up to a tile that divides the page
     while (d->page_size % a.box) a.box >>= 1;
+    a.grouped = a.box >= kGroupRows;
     a.num_pages = d->num_pages;
     a.max_pages = d->max_pages_per_req;
     a.cost_max = T > a.tpq ? kCost2 : kCost1;
