@@ -64,6 +64,9 @@ constexpr int kChunkThreads = 384;
 constexpr int kLaunchRegs = 168, kRegsLow = 88, kRegsHigh = 208;
 static_assert(kRegsLow * 128 + kRegsHigh * 256 <= kLaunchRegs * kChunkThreads, "register split exceeds the launch");
 
+// Pairs of 16 whose weights the polynomial takes.
+constexpr uint32_t kPolyPairs = 0x4924;
+
 // A cut item, for the joining kernel (written by the CTA with its first keys).
 struct ChunkCut {
     int parts;  // CTAs that hold a part, from the writing one on; 0: nothing cut
@@ -157,6 +160,7 @@ struct Piece {
     int mode;            // two row tiles, one, or one of at most 32 rows
     int slot;            // of the partial result, -1 for a whole item
     int merged;          // the new tokens lie in the last cached tile
+    int items;           // of the request's KV head
 };
 constexpr int kPieces = 16;  // pieces that the roles may lie apart
 
@@ -164,7 +168,9 @@ template <int D>
 struct ChunkShape {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = kHalves * kHalfBytes;  // bytes of a Q, K or V tile
-    static constexpr int kStages = D == 128 ? 5 : 10;   // ring of K and V tiles
+    // rings of K and V tiles; a V tile is held longer (until P.V, after its softmax)
+    static constexpr int kStagesK = D == 128 ? 2 : 5, kStagesV = D == 128 ? 3 : 5;
+    static constexpr int kStages = kStagesK + kStagesV;
     static constexpr int kControl = 3072;
     static constexpr size_t kSmem() { return (size_t)(2 + kStages) * kTile + kControl; }
 };
@@ -183,7 +189,7 @@ struct ChunkShared {
     uint32_t tmem;
     int abort_flag, never;
     uint32_t published;  // pieces written by the producer
-    uint32_t issued;     // ring positions that the producer has begun to fill
+    uint32_t issued[2];  // K, V tiles that their producer has begun to load
     uint32_t fixed;      // pieces that the fixing warp is done with
     uint32_t epilogues[2];  // finished by the warps of a softmax warpgroup (4 a piece)
     int bad_piece;       // the piece whose `bad_from` holds, or -1
@@ -195,6 +201,14 @@ ISD_DEVINL float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// A weight may be taken by the special-function unit (ex2, 16 a clock and SM,
+// which alone would hold a tile of 128 rows for 1024 cycles) or by this
+// polynomial on the FMA pipes: 2^x = 2^n 2^f, n = round(x), |f| <= 1/2, 2^f by
+// a minimax polynomial of degree 4 with 2^0 = 1 (found by iteratively weighted
+// least squares; relative error 2.9e-6).  x is held in [-127, 127]: below, the
+// result is exactly 0; a larger x comes out as 2^127 and a NaN as a large value.
+constexpr float kEx1 = 0.693124175f, kEx2 = 0.240240991f, kEx3 = 0.0559064262f, kEx4 = 0.00958285295f;
 
 // two 32-bit operations at once
 ISD_DEVINL unsigned long long pair(float lo, float hi) {
@@ -214,6 +228,30 @@ ISD_DEVINL unsigned long long add2(unsigned long long a, unsigned long long b) {
     unsigned long long r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+
+ISD_DEVINL float clamp127(float x) {  // NaN stays NaN
+    float y;
+    asm("{\n .reg .f32 t;\n max.NaN.f32 t, %1, 0fC2FE0000;\n min.NaN.f32 %0, t, 0f42FE0000;\n}\n" : "=f"(y) : "f"(x));
+    return y;
+}
+ISD_DEVINL unsigned long long ex2_poly(unsigned long long v) {
+    float x, y;
+    unpair(v, x, y);
+    const unsigned long long xx = pair(clamp127(x), clamp127(y));
+    const unsigned long long magic = pair(12582912.f, 12582912.f);  // 1.5 2^23: adding it rounds to an integer
+    const unsigned long long t = add2(xx, magic);
+    const unsigned long long n = add2(t, pair(-12582912.f, -12582912.f));
+    const unsigned long long f = fma2(n, pair(-1.f, -1.f), xx);
+    unsigned long long r = fma2(f, pair(kEx4, kEx4), pair(kEx3, kEx3));
+    r = fma2(r, f, pair(kEx2, kEx2));
+    r = fma2(r, f, pair(kEx1, kEx1));
+    r = fma2(r, f, pair(1.f, 1.f));
+    float tx, ty;
+    unpair(t, tx, ty);
+    unpair(r, x, y);
+    return pair(__int_as_float(__float_as_int(x) + (__float_as_int(tx) << 23)),
+                __int_as_float(__float_as_int(y) + (__float_as_int(ty) << 23)));
 }
 
 ISD_DEVINL void tmem_st32(uint32_t taddr, const uint32_t* r) {
@@ -278,16 +316,6 @@ ISD_DEVINL void mbar_arrive_n(uint64_t* bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
 
-// box of whole 8-row groups of a page with all of a head's dimensions
-ISD_DEVINL void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int half, int group, int page,
-                            uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%3, %3, %4, %5, %6}], [%2], %7;\n" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(smem_u32(bar)), "r"(0), "r"(half), "r"(group), "r"(page), "l"(policy)
-        : "memory");
-}
-
 ISD_DEVINL uint64_t policy_evict_normal() {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(p));
@@ -321,7 +349,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
              const __grid_constant__ ChunkArgs a) {
     using namespace sm100;
     using Shape = ChunkShape<D>;
-    constexpr int NH = Shape::kHalves, NST = Shape::kStages;
+    constexpr int NH = Shape::kHalves, NST = Shape::kStages, NK = Shape::kStagesK, NV = Shape::kStagesV;
     constexpr uint32_t kTmemCols = 512, kTmemO = 256;
     extern __shared__ __align__(1024) unsigned char smem_raw[];  // there is no other shared memory
     unsigned char* sQ = smem_raw;
@@ -349,7 +377,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         mbar_init(&sh->meet, 8);
         mbar_init(&sh->drain, 1);
         sh->abort_flag = sh->never = 0;
-        sh->published = sh->issued = sh->fixed = sh->epilogues[0] = sh->epilogues[1] = 0;
+        sh->published = sh->issued[0] = sh->issued[1] = sh->fixed = sh->epilogues[0] = sh->epilogues[1] = 0;
         sh->bad_piece = -1;
         sh->b = a.B;
         fence_mbar_init();
@@ -490,7 +518,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const uint32_t q_at = smem_u32(sQ) >> 4, ring_at = smem_u32(ring) >> 4;
                 struct Cursor {
                     uint32_t st, ph;  // ring stage and parity of the next K (V) tile
-                } kc = {0, 0}, vc = {1, 0};
+                } kc = {0, 0}, vc = {NK, 0};
                 uint32_t fixes = 0;       // per stage: parity of the next fix
                 uint32_t q_ph = 0, p_ph = 0, ones = 0;  // parities: bit by Q slot, by warpgroup
                 bool ok = true;
@@ -512,16 +540,15 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     return good;
                 };
                 // the next K (V) tile is there, and fixed: its stage
-                auto take = [&](Cursor& c, bool fixed, uint32_t& stage) {
+                auto take = [&](Cursor& c, bool is_v, bool fixed, uint32_t& stage) {
                     stage = c.st;
                     if (!wait(&sh->full[c.st], c.ph)) return false;
                     if (fixed) {
                         if (!wait(&sh->fix[c.st], fixes >> c.st)) return false;
                         fixes ^= 1u << c.st;
                     }
-                    c.st += 2;
-                    if (c.st >= NST) {
-                        c.st -= NST;
+                    if (++c.st == (is_v ? NST : NK)) {
+                        c.st = is_v ? NK : 0;
                         c.ph ^= 1;
                     }
                     tc_fence_after();
@@ -550,7 +577,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     for (int kk = 0; kk < kKeys / 16; ++kk)
                         mma_ts(tmem + kTmemO + w * D, tmem + w * kKeys + kk * 8, v + kk * step, hi, idesc_o,
                                !(first && kk == 0));
-                    commit_to(&sh->pv_done[w]);
                 };
                 Piece p;
                 for (uint32_t n = 0; ok && __all_sync(0xffffffffu, piece_at(n, p)); ++n) {
@@ -565,7 +591,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     // S(k + ...) overwrites P(k), which the product issued before it
                     // reads: the tensor core takes them in this order
                     if (p.mode == kTwo) {
-                        if (!wait_q(0) || !wait_q(1) || !take(kc, k_fix == 0, ks)) break;
+                        if (!wait_q(0) || !wait_q(1) || !take(kc, false, k_fix == 0, ks)) break;
                         s_product(0, 0, ks, grouped(0));
                         s_product(1, 1, ks, grouped(0));
                         free_stage(ks);
@@ -573,27 +599,25 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll 1
                         for (int k = 0; k < nt; ++k) {
                             const bool more = k + 1 < nt;
-                            if (!take(vc, v_fixed(k), vs) || !wait_p(0)) break;
-                            pv_product(0, vs, grouped(k), k == 0);
-                            if (more) {
-                                if (!take(kc, k + 1 == k_fix, ks)) break;
-                                s_product(0, 0, ks, grouped(k + 1));
+                            if (!take(vc, true, v_fixed(k), vs) || (more && !take(kc, false, k + 1 == k_fix, ks))) break;
+#pragma unroll 1
+                            for (int w = 0; w < 2; ++w) {
+                                if (!wait_p(w)) break;
+                                pv_product(w, vs, grouped(k), k == 0);
+                                if (more) s_product(w, w, ks, grouped(k + 1));
                             }
-                            if (!wait_p(1)) break;
-                            pv_product(1, vs, grouped(k), k == 0);
                             free_stage(vs);
-                            if (more) {
-                                s_product(1, 1, ks, grouped(k + 1));
-                                free_stage(ks);
-                            }
+                            if (more) free_stage(ks);
                         }
-                        commit_to(&sh->q_empty[0]);
-                        commit_to(&sh->q_empty[1]);
+                        for (int w = 0; w < 2; ++w) {
+                            commit_to(&sh->pv_done[w]);
+                            commit_to(&sh->q_empty[w]);
+                        }
                     } else {
                         const int qs = ones++ & 1;
                         auto s_next = [&](int k) {
                             if (k >= nt) return true;
-                            if (!take(kc, k == k_fix, ks)) return false;
+                            if (!take(kc, false, k == k_fix, ks)) return false;
                             s_product(k & 1, qs, ks, grouped(k));
                             free_stage(ks);
                             return true;
@@ -602,9 +626,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         if (!wait(&sh->o_free[0], n + 1) || !wait(&sh->o_free[1], n + 1)) break;
 #pragma unroll 1
                         for (int k = 0; k < nt; ++k) {
-                            if (!take(vc, v_fixed(k), vs) || !wait_p(k & 1)) break;
+                            if (!take(vc, true, v_fixed(k), vs) || !wait_p(k & 1)) break;
                             pv_product(k & 1, vs, grouped(k), k < 2);
                             free_stage(vs);
+                            if (k + 2 >= nt) commit_to(&sh->pv_done[k & 1]);
                             if (!s_next(k + 2)) break;
                         }
                     }
@@ -612,15 +637,19 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 commit_to(&sh->drain);
                 mbar_wait_bounded(&sh->drain, 0, &sh->never, kWaitNs);
             }
-        } else if (warp == 9) {
-            // ------------------------------------------------ TMA producer
-            // walks the CTA's range (order: request, KV head, item), publishes
-            // its pieces to the other roles and loads their tiles
+        } else if (warp <= 10) {
+            // ------------------------------------------------ TMA producers
+            // Warp 9 walks the CTA's range (order: request, KV head, item),
+            // publishes its pieces to the other roles and loads Q and the K tiles;
+            // warp 10 loads the V tiles.
+            const bool is_v = warp == 10;
             const uint64_t pol = policy_evict_normal(), pol_first = policy_evict_first();
-            uint32_t pos = 0, n = 0, q_use[2] = {0, 0}, ones = 0;
-            const int nb = kKeys / a.box, boxes = a.grouped ? nb : nb * NH;  // boxes of a cached tile
-            const int x_half = lane / nb, x_row = (lane - x_half * nb) * a.box;
-            const bool one_each = boxes <= 32;  // else the boxes' pages are looked up as they go
+            uint32_t st = is_v ? NK : 0, ph = 0, armed = 0, armed_ph = 0;  // the next tile's stage and parity; stages loaded into
+            uint32_t tiles = 0, n = 0, q_use[2] = {0, 0}, ones = 0;
+            const int nb = kKeys / a.box;  // boxes of a cached tile (of each 64-d half, when not grouped)
+            const int x_row = (lane < nb ? lane : 0) * a.box;
+            const int tile_pages = kKeys / a.P, tile_rest = kKeys % a.P;
+            const int none = (int)((long long)a.num_pages * a.P / kGroupRows);  // the group past the last: reads as zeros
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t par) {
                 if (lane == 0 && !mbar_wait_bounded(bar, par & 1, abort_flag, kWaitNs)) {
@@ -643,17 +672,18 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     *(volatile uint32_t*)&sh->published = n + 1;
                 }
                 __syncwarp();
-                ++n;
             };
             int b = bad ? a.B : sh->b, g = sh->g, q = sh->q, rel = sh->rel;  // rel: the item's start less my0
             const int len = sh->len;
             Request r = sh->first;
-            Piece p = {};
-            while (ok && b < a.B && rel < len) {
-                const Item it = item_of(a, r, q);
-                p.t0 = rel >= 0 ? 0 : (it.two ? (-rel + kCost2 - 1) / kCost2 : (-rel + kCost1 - 1) / kCost1);
-                p.t1 = min(it.nt, it.two ? (len - rel + kCost2 - 1) / kCost2 : (len - rel + kCost1 - 1) / kCost1);
-                if (p.t0 < p.t1) {
+            // the next piece of the walk; one without tiles at its end
+            auto walk = [&](Piece& p) {
+                p.t0 = p.t1 = 0;
+                while (b < a.B && rel < len) {
+                    const Item it = item_of(a, r, q);
+                    const int start = rel;
+                    if (start < 0) p.t0 = it.two ? (-start + kCost2 - 1) / kCost2 : (-start + kCost1 - 1) / kCost1;
+                    p.t1 = min(it.nt, it.two ? (len - start + kCost2 - 1) / kCost2 : (len - start + kCost1 - 1) / kCost1);
                     p.b = b;
                     p.g = g;
                     p.start = r.start;
@@ -664,155 +694,135 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     p.mode = it.two ? kTwo : it.i1 - it.i0 <= a.tps ? kQuad : kOne;
                     p.slot = p.t0 > 0 ? 0 : p.t1 < it.nt ? 1 : -1;
                     p.merged = r.merged;
-                    // box x = lane + 32 j of a cached tile: rows from (x % nb) * box
-                    // on, of 64-d half x / nb (of both when grouped).  The pages of
-                    // the next tile are fetched while this one is loaded.
-                    const int32_t* table = a.page_table + (size_t)b * a.max_pages;
-                    auto page_of = [&](int key) {
-                        int page = -1;  // a page past the cached keys, or a bad one, reads as zeros
-                        if (key < r.kv) {
-                            page = __ldg(table + key / a.P);
-                            if (page < 0 || page >= a.num_pages) {
-                                raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
-                                page = -1;
-                            }
+                    p.items = r.items;
+                    // the next item
+                    rel += it.cost;
+                    if (++q >= r.items) {
+                        q = 0;
+                        if (++g >= a.Hkv) {
+                            g = 0;
+                            do {
+                                if (++b >= a.B) break;
+                                r = request_of(a, a.q_start[b], a.q_start[b + 1], a.kv_len[b]);
+                            } while (r.items == 0);
                         }
-                        return page;
-                    };
-                    int next_page = -1, next_in = 0;
-                    if (one_each && p.t0 < r.kvt) {
-                        next_page = page_of(p.t0 * kKeys + x_row);
-                        next_in = (p.t0 * kKeys + x_row) % a.P;
                     }
+                    if (p.t0 < p.t1) {
+                        if (p.slot == 1 && lane == 0) {
+                            // CTAs that hold a part: this one to the owner of the item's last tile
+                            const long long most = sh->total / a.cost_max;
+                            const int G = (int)min((long long)gridDim.x, max(most, 1ll));
+                            const long long last_at = sh->my0 + start + (long long)(it.nt - 1) * it.w;
+                            const int last = (int)(((last_at + 1) * G - 1) / sh->total);
+                            ChunkCut c = {last - (int)blockIdx.x + 1, p.g, it.i0, it.i1, p.start, {0, 0, 0}};
+                            a.cuts[blockIdx.x] = c;
+                        }
+                        return;
+                    }
+                    p.t0 = p.t1 = 0;
+                }
+            };
+            for (; ok; ++n) {
+                Piece p;
+                if (is_v) {
+                    if (!__all_sync(0xffffffffu, piece_at(n, p))) break;
+                } else {
+                    walk(p);
                     publish(p);
-                    if (!ok) break;
-                    const int q0 = it.two ? 0 : ones++ & 1, q1 = it.two ? 1 : q0;
+                    if (!ok || p.t0 >= p.t1) break;
+                    const bool two = p.mode == kTwo;
+                    const int q0 = two ? 0 : ones++ & 1, q1 = two ? 1 : q0;
                     for (int s = q0; s <= q1; ++s) {
                         if (!wait(&sh->q_empty[s], q_use[s] + 1)) break;
                         ++q_use[s];
                         if (lane == 0) {
                             unsigned char* dst = sQ + s * Shape::kTile;
-                            const int row0 = r.start + it.i0 + (s - q0) * a.tpq;
+                            const int row0 = p.start + p.i0 + (s - q0) * a.tpq;
                             if (p.mode == kQuad) {
                                 mbar_arrive_expect_tx(&sh->q_full[s], (uint32_t)(4 * a.tps * a.grp * 128 * NH));
+#pragma unroll 1
                                 for (int x = 0; x < 4 * NH; ++x)
                                     tma_load_4d(dst + (x >> 2) * kHalfBytes + (x & 3) * 32 * 128, &tm_qs,
-                                                &sh->q_full[s], 64 * (x >> 2), g * a.grp, row0, 0, pol);
+                                                &sh->q_full[s], 64 * (x >> 2), p.g * a.grp, row0, 0, pol);
                             } else {
                                 mbar_arrive_expect_tx(&sh->q_full[s], (uint32_t)(a.tpq * a.grp * 128 * NH));
+#pragma unroll 1
                                 for (int h = 0; h < NH; ++h)
-                                    tma_load_4d(dst + h * kHalfBytes, &tm_q, &sh->q_full[s], 64 * h, g * a.grp, row0,
+                                    tma_load_4d(dst + h * kHalfBytes, &tm_q, &sh->q_full[s], 64 * h, p.g * a.grp, row0,
                                                 0, pol_first);
                             }
                         }
                     }
-                    // keys that only this item reads need not stay in L2
-                    const uint64_t pol_kv = r.items == 1 ? pol_first : pol;
-                    for (int t = p.t0; ok && t < p.t1; ++t) {
-                        const int page = next_page, in = next_in;
-                        if (one_each && t + 1 < p.t1 && t + 1 < r.kvt) {
-                            next_page = page_of((t + 1) * kKeys + x_row);
-                            next_in = ((t + 1) * kKeys + x_row) % a.P;
-                        }
-                        for (int v = 0; v < 2; ++v, ++pos) {
-                            const uint32_t s = pos % NST;
-                            if (!wait(&sh->empty[s], pos / NST + 1)) break;
-                            unsigned char* dst = ring + s * Shape::kTile;
-                            if (lane == 0) {
-                                mbar_arrive_expect_tx(&sh->full[s], Shape::kTile);
-                                *(volatile uint32_t*)&sh->issued = pos + 1;
-                            }
-                            __syncwarp();
-                            if (t >= r.kvt) {
-                                if (lane < NH)
-                                    tma_load_4d(dst + lane * kHalfBytes, v ? &tm_vn : &tm_kn, &sh->full[s], 64 * lane,
-                                                g, r.start + (t - r.kvt) * kKeys, 0, pol);
-                            } else if (a.grouped) {
-                                if (lane < nb)
-                                    tma_load_5d(dst + x_row * 128 * NH, v ? &tm_v : &tm_k, &sh->full[s], g * NH,
-                                                in / kGroupRows, page, pol_kv);
-                            } else if (one_each) {
-                                if (lane < boxes)
-                                    tma_load_4d(dst + x_half * kHalfBytes + x_row * 128, v ? &tm_v : &tm_k, &sh->full[s],
-                                                64 * x_half, g, in, page, pol_kv);
-                            } else {
-                                for (int x = lane; x < boxes; x += 32) {
-                                    const int h = x / nb, row = (x - h * nb) * a.box, key = t * kKeys + row;
-                                    tma_load_4d(dst + h * kHalfBytes + row * 128, v ? &tm_v : &tm_k, &sh->full[s],
-                                                64 * h, g, key % a.P, page_of(key), pol_kv);
-                                }
-                            }
-                        }
+                }
+                // lane x holds the page of box x, rows from x * box on, of a
+                // grouped tile (keys past the cached ones have none; such a page,
+                // like a bad one, reads as zeros); the next tile's is fetched while
+                // one is loaded
+                const int32_t* table = a.page_table + (size_t)p.b * a.max_pages;
+                auto checked = [&](int page) {
+                    if (page >= 0 && page < a.num_pages) return page;
+                    raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
+                    return -1;
+                };
+                int key = p.t0 * kKeys + x_row, at = key / a.P, in = key - at * a.P, page = 0;
+                if (a.grouped && key < p.kv) page = __ldg(table + at);
+                // keys that only this item reads need not stay in L2
+                const uint64_t pol_kv = p.items == 1 ? pol_first : pol;
+                const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+#pragma unroll 1
+                for (int t = p.t0; t < p.t1; ++t) {
+                    int group = none;
+                    if (key < p.kv && a.grouped) {
+                        const int id = checked(page);
+                        if (id >= 0) group = (int)(((long long)id * a.P + in) / kGroupRows);
                     }
-                    if (p.slot == 1 && lane == 0) {
-                        // CTAs that hold a part: this one to the owner of the item's last tile
-                        const long long most = sh->total / a.cost_max;
-                        const int G = (int)min((long long)gridDim.x, max(most, 1ll));
-                        const long long last_at = sh->my0 + rel + (long long)(it.nt - 1) * it.w;
-                        const int last = (int)(((last_at + 1) * G - 1) / sh->total);
-                        ChunkCut c = {last - (int)blockIdx.x + 1, g, it.i0, it.i1, r.start, {0, 0, 0}};
-                        a.cuts[blockIdx.x] = c;
+                    if (a.grouped && t + 1 < p.t1) {
+                        key += kKeys;
+                        at += tile_pages;
+                        in += tile_rest;
+                        if (in >= a.P) {
+                            in -= a.P;
+                            ++at;
+                        }
+                        if (key < p.kv) page = __ldg(table + at);
+                    }
+                    if (!wait(&sh->empty[st], ph ^ 1)) break;
+                    unsigned char* dst = ring + st * Shape::kTile;
+                    uint64_t* bar = &sh->full[st];
+                    ++tiles;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar, Shape::kTile);
+                        *(volatile uint32_t*)&sh->issued[is_v] = tiles;
+                    }
+                    armed |= 1u << st;
+                    armed_ph = (armed_ph & ~(1u << st)) | ph << st;
+                    if (++st == (is_v ? NST : NK)) {
+                        st = is_v ? NK : 0;
+                        ph ^= 1;
+                    }
+                    __syncwarp();
+                    if (t >= p.kvt) {
+                        if (lane < NH)
+                            tma_load_4d(dst + lane * kHalfBytes, is_v ? &tm_vn : &tm_kn, bar, 64 * lane, p.g,
+                                        p.start + (t - p.kvt) * kKeys, 0, pol);
+                    } else if (a.grouped) {
+                        if (lane < nb)
+                            tma_load_4d(dst + x_row * (128 * NH), map, bar, 0, 0, p.g * NH, group, pol_kv);
+                    } else {
+                        for (int x = lane; x < nb * NH; x += 32) {
+                            const int h = x / nb, row = (x - h * nb) * a.box, k = t * kKeys + row;
+                            tma_load_4d(dst + h * kHalfBytes + row * 128, map, bar, 64 * h, p.g, k % a.P,
+                                        k < p.kv ? checked(__ldg(table + k / a.P)) : -1, pol_kv);
+                        }
                     }
                 }
-                // the next item
-                rel += it.cost;
-                if (++q < r.items) continue;
-                q = 0;
-                if (++g < a.Hkv) continue;
-                g = 0;
-                do {
-                    if (++b >= a.B) break;
-                    r = request_of(a, a.q_start[b], a.q_start[b + 1], a.kv_len[b]);
-                } while (r.items == 0);
             }
-            p.t0 = p.t1 = 0;
-            if (ok) publish(p);
             // drain: every copy has landed before the CTA may exit
             if (lane == 0) {
-                for (uint32_t i = pos > NST ? pos - NST : 0; i < pos; ++i)
-                    mbar_wait_bounded(&sh->full[i % NST], (i / NST) & 1, &sh->never, kWaitNs);
+                for (int s = 0; s < NST; ++s)
+                    if (armed >> s & 1) mbar_wait_bounded(&sh->full[s], armed_ph >> s & 1, &sh->never, kWaitNs);
                 for (int s = 0; s < 2; ++s)
                     if (q_use[s]) mbar_wait_bounded(&sh->q_full[s], (q_use[s] - 1) & 1, &sh->never, kWaitNs);
-            }
-        } else if (warp == 10) {
-            // ------------------------------------------------ append
-            // this CTA's share of the new rows, each to its page, 16 bytes a lane
-            const int t0 = bad ? 0 : (int)((long long)a.T * blockIdx.x / gridDim.x);
-            const int t1 = bad ? 0 : (int)((long long)a.T * (blockIdx.x + 1) / gridDim.x);
-            if (t0 < t1) {
-                int lo = -1, hi = a.B;  // the last request that starts at or before t0
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (a.q_start[mid] <= t0) lo = mid; else hi = mid;
-                }
-                int b = lo;
-                for (int t = t0; t < t1; ++t) {
-                    while (b + 1 < a.B && a.q_start[b + 1] <= t) ++b;
-                    if (b < 0 || t >= a.q_start[b + 1]) continue;  // a row of no request
-                    const int start = a.q_start[b], kv = a.kv_len[b];
-                    if (chunk_tokens(a, kv, a.q_start[b + 1] - start) == 0) {
-                        if (lane == 0) raise_flag(a.err_flag, ISD_FLAG_CAPACITY);
-                        uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)t * a.Hq * D);
-                        for (int i = lane; i < a.Hq * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
-                    const int at = kv + (t - start);
-                    const int page = a.page_table[(size_t)b * a.max_pages + at / a.P];
-                    if (page < 0 || page >= a.num_pages) {
-                        if (lane == 0) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
-                        continue;
-                    }
-                    const size_t dst = ((size_t)page * a.P + at % a.P) * a.Hkv * D, src = (size_t)t * a.Hkv * D;
-                    const uint4* ks = reinterpret_cast<const uint4*>(a.k_new + src);
-                    const uint4* vs = reinterpret_cast<const uint4*>(a.v_new + src);
-                    uint4* kd = reinterpret_cast<uint4*>(a.k_pool + dst);
-                    uint4* vd = reinterpret_cast<uint4*>(a.v_pool + dst);
-#pragma unroll 4
-                    for (int i = lane; i < a.Hkv * D / 8; i += 32) {
-                        kd[i] = __ldg(ks + i);
-                        vd[i] = __ldg(vs + i);
-                    }
-                }
             }
         } else {
             // ------------------------------------------------ tiles that need a touch
@@ -820,19 +830,66 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             // are zeroed in V (0 * NaN would spoil the sum), the new tokens of a
             // merged tile are put into their rows, and infinities and NaN in V
             // rows that only some of the item's rows see are taken out and noted
-            // for the epilogue.
-            uint32_t rc = 0, n = 0;
+            // for the epilogue.  Between them, and at the end, this warp appends its
+            // CTA's share of the new rows to their pages, a token at a time.
+            uint32_t tiles = 0, n = 0;  // key tiles of the pieces before; pieces
             bool ok = true;
             auto all_ok = [&](bool good) {
                 ok = __all_sync(0xffffffffu, good);
                 return ok;
             };
-            // the tile at ring position pos has landed.  This warp skips most
-            // positions, so it first waits until the producer is at this one: the
-            // barrier's phase is then the tile's, and stays it until the fix.
-            auto landed = [&](uint32_t pos) {
-                if (!all_ok(until(&sh->issued, pos + 1))) return false;
-                const bool good = mbar_wait_bounded(&sh->full[pos % NST], (pos / NST) & 1, abort_flag, kWaitNs);
+            int t_new = bad ? 0 : (int)((long long)a.T * blockIdx.x / gridDim.x), b_new = -2;
+            const int t_end = bad ? 0 : (int)((long long)a.T * (blockIdx.x + 1) / gridDim.x);
+            auto append = [&]() {
+                const int t = t_new++;
+                if (b_new == -2) {  // the last request that starts at or before t
+                    int hi = a.B;
+                    b_new = -1;
+                    while (hi - b_new > 1) {
+                        const int mid = (b_new + hi) >> 1;
+                        if (a.q_start[mid] <= t) b_new = mid; else hi = mid;
+                    }
+                }
+                while (b_new + 1 < a.B && a.q_start[b_new + 1] <= t) ++b_new;
+                const int b = b_new;
+                if (b < 0 || t >= a.q_start[b + 1]) return;  // a row of no request
+                const int start = a.q_start[b], kv = a.kv_len[b];
+                if (chunk_tokens(a, kv, a.q_start[b + 1] - start) == 0) {
+                    if (lane == 0) raise_flag(a.err_flag, ISD_FLAG_CAPACITY);
+                    uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)t * a.Hq * D);
+                    for (int i = lane; i < a.Hq * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+                    return;
+                }
+                const int at = kv + (t - start);
+                const int page = a.page_table[(size_t)b * a.max_pages + at / a.P];
+                if (page < 0 || page >= a.num_pages) {
+                    if (lane == 0) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
+                    return;
+                }
+                const size_t dst = ((size_t)page * a.P + at % a.P) * a.Hkv * D, src = (size_t)t * a.Hkv * D;
+                const uint4* ks = reinterpret_cast<const uint4*>(a.k_new + src);
+                const uint4* vs = reinterpret_cast<const uint4*>(a.v_new + src);
+                uint4* kd = reinterpret_cast<uint4*>(a.k_pool + dst);
+                uint4* vd = reinterpret_cast<uint4*>(a.v_pool + dst);
+#pragma unroll 4
+                for (int i = lane; i < a.Hkv * D / 8; i += 32) {
+                    kd[i] = __ldg(ks + i);
+                    vd[i] = __ldg(vs + i);
+                }
+            };
+            // until() with appending for a pastime
+            auto meanwhile = [&](const uint32_t* counter, uint32_t least) {
+                while (t_new < t_end && !__any_sync(0xffffffffu, peek(counter) >= least)) append();
+                return all_ok(until(counter, least));
+            };
+            // The tile (K: v = 0, V: v = 1) number `tile` of this CTA has landed.
+            // This warp skips most, so it first waits until the producer is at
+            // this one: the barrier's phase is then the tile's, and stays it until
+            // the fix.
+            auto landed = [&](int v, uint32_t tile) {
+                if (!meanwhile(&sh->issued[v], tile + 1)) return false;
+                const uint32_t s = v ? NK + tile % NV : tile % NK, round = v ? tile / NV : tile / NK;
+                const bool good = mbar_wait_bounded(&sh->full[s], round & 1, abort_flag, kWaitNs);
                 if (!good) give_up();
                 return all_ok(good);
             };
@@ -873,22 +930,22 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 return true;
             };
             Piece p;
-            while (all_ok(piece_at(n, p))) {
+            while (meanwhile(&sh->published, n + 1) && all_ok(piece_at(n, p))) {
                 // the cached tile with free rows, and the new tiles that some row does not see whole
                 if (p.kv % kKeys && p.t0 < p.kvt && p.t1 >= p.kvt) {
-                    const uint32_t kp = rc + 2 * (p.kvt - 1 - p.t0), vp = kp + 1;
-                    const uint32_t ks = kp % NST, vs = vp % NST;
+                    const uint32_t tile = tiles + (p.kvt - 1 - p.t0);
+                    const uint32_t ks = tile % NK, vs = NK + tile % NV;
                     const int m = p.kv % kKeys;  // cached keys of the tile
                     // the item's new tokens (a row of an item sees none past its last)
                     const int fresh = p.merged ? p.i1 : 0;
                     if (fresh) {
-                        if (!landed(kp)) break;
+                        if (!landed(0, tile)) break;
                         for (int i = r_in; i < fresh; i += kRowsStep)
                             *cell(ks, m + i, a.grouped) = __ldg(
                                 reinterpret_cast<const uint4*>(a.k_new + ((size_t)(p.start + i) * a.Hkv + p.g) * D) + ch);
                         done(ks);
                     }
-                    if (!landed(vp)) break;
+                    if (!landed(1, tile)) break;
                     for (int i0 = 0; i0 < fresh; i0 += kRowsStep) {
                         const int i = i0 + r_in;
                         uint4 w = make_uint4(0, 0, 0, 0);
@@ -911,8 +968,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 for (int t = first; ok && t < p.t1; ++t) {
                     const int base = (t - p.kvt) * kKeys;
                     if (base + kKeys <= p.i0 + 1) continue;  // every row sees all of it
-                    const uint32_t vp = rc + 2 * (t - p.t0) + 1, vs = vp % NST;
-                    if (!landed(vp)) break;
+                    const uint32_t tile = tiles + (t - p.t0), vs = NK + tile % NV;
+                    if (!landed(1, tile)) break;
                     const int rows = min(kKeys, p.i1 - base);
                     for (int r0 = max(0, p.i0 + 1 - base); r0 < rows; r0 += kRowsStep) {
                         const int row = r0 + r_in;
@@ -930,10 +987,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     done(vs);
                 }
                 if (!ok) break;
-                rc += 2 * (p.t1 - p.t0);
+                tiles += p.t1 - p.t0;
                 ++n;
                 if (lane == 0) *(volatile uint32_t*)&sh->fixed = n;
             }
+            while (t_new < t_end) append();
         }
     } else {
         setmaxnreg_inc<kRegsHigh>();
@@ -941,7 +999,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         const int wg = warp >> 2, wq = warp & 3;  // warpgroup; its warp, a quarter of the TMEM lanes
         const uint32_t tm_lane = tmem + ((uint32_t)(wq * 32) << 16);
         const uint32_t tm_s = tm_lane + wg * kKeys, tm_o = tm_lane + kTmemO;
-        uint32_t s_use = 0, pvs = 0, ones = 0, met = 0;
+        uint32_t s_use = 0, o_use = 0, ones = 0, met = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t par) {
             const bool good = mbar_wait_bounded(bar, par & 1, abort_flag, kWaitNs);
@@ -954,14 +1012,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->meet);
             return wait(&sh->meet, met++);
-        };
-        // The latest product of this warpgroup is done.  Every product is waited
-        // for before the next one's weights are handed over, so the barrier is
-        // never two phases away.
-        auto pv_wait = [&]() {
-            if (!wait(&sh->pv_done[wg], pvs - 1)) return false;
-            tc_fence_after();
-            return true;
         };
         Piece p;
         for (uint32_t n = 0; ok && __all_sync(0xffffffffu, piece_at(n, p)); ++n) {
@@ -977,7 +1027,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const float m_new = fmaxf(m_ref, top);
                 const float f = m_new > m_ref ? ex2(m_ref - m_new) : 1.f;
                 if (has_o) {
-                    if (!pv_wait()) return;
 #pragma unroll 1
                     for (int j = 0; j < D; j += 16) {
                         uint32_t o[16];
@@ -992,8 +1041,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 l *= f;
                 m_ref = m_new;
             };
-            auto hide = [&](float (&s)[32], int seen) {  // scores from `seen` on
-                if (__any_sync(0xffffffffu, seen < 32)) {
+            auto hide = [&](float (&s)[32], bool some, int seen) {  // scores from `seen` on
+                if (some) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (j >= seen) s[j] = -INFINITY;
@@ -1008,22 +1057,31 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 }
                 return fmaxf(x, y);
             };
-            // weights of 32 scores: rounded to bf16 for the product with V, summed in 32 bits
-            auto weights = [&](const float (&s)[32], float mu, unsigned long long& sum, uint32_t* w) {
+            // weights of 32 scores: rounded to bf16 for the product with V, summed
+            // in 32 bits; the pairs in `poly` by the polynomial
+            auto weights = [&](const float (&s)[32], float mu, unsigned long long& sum, uint32_t* w, uint32_t poly) {
                 const unsigned long long sc = pair(a.scale_log2, a.scale_log2), neg = pair(-mu, -mu);
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
+                for (int j = 0; j < 16; ++j) {
+                    unsigned long long v = fma2(pair(s[2 * j], s[2 * j + 1]), sc, neg);
                     float x, y;
-                    unpair(fma2(pair(s[j], s[j + 1]), sc, neg), x, y);
-                    x = ex2(x);
-                    y = ex2(y);
-                    sum = add2(sum, pair(x, y));
-                    w[j >> 1] = pack_bf16(x, y);
+                    if (poly >> j & 1) {
+                        v = ex2_poly(v);
+                        unpair(v, x, y);
+                    } else {
+                        unpair(v, x, y);
+                        x = ex2(x);
+                        y = ex2(y);
+                        v = pair(x, y);
+                    }
+                    sum = add2(sum, v);
+                    w[j] = pack_bf16(x, y);
                 }
             };
             for (int t = t_first; t < p.t1; t += step) {
                 if (!wait(&sh->s_full[wg], s_use++)) break;
                 tc_fence_after();
+                // (S is here, so the warpgroup's product before it is done too)
                 // keys of this tile that the row sees
                 int seen;
                 if (t < p.kvt) {
@@ -1033,87 +1091,100 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     seen = i + 1 - (t - p.kvt) * kKeys;
                 }
                 if (!live) seen = 0;
-                const bool has_o = t != t_first;
+                const bool has_o = t != t_first, some = __any_sync(0xffffffffu, seen < kKeys);
                 // Weights are taken by the reference as it is.  Only when a row's sum
-                // of them passes 2^10 (then one may be large) is its maximum looked
-                // up and the reference moved, and they are done over: S is still there.
+                // of them passes 2^10 (then one may be large), or is none, is its
+                // maximum looked up and the reference moved, and they are done over:
+                // S is still there.
                 float sum;
                 if (quad) {
                     // a quarter of the keys: the row's other quarters are other warps'
                     float s[32];
                     tmem_ld32(tm_s + wq * 32, s);
                     tmem_arrived(s);
-                    hide(s, seen - wq * 32);
+                    hide(s, some, seen - wq * 32);
                     if (!has_o) move_ref(top_of(s) * a.scale_log2, false);
                     uint32_t w[16];
                     for (;;) {
                         unsigned long long acc = 0;
-                        weights(s, m_ref == -INFINITY ? 0.f : m_ref, acc, w);
+                        weights(s, m_ref == -INFINITY ? 0.f : m_ref, acc, w, 0);
                         float y;
                         unpair(acc, sum, y);
                         sum += y;
                         if (!__any_sync(0xffffffffu, sum > 1024.f)) break;
                         move_ref(top_of(s) * a.scale_log2, has_o);
-                        if (!ok) break;
                     }
-                    if (!ok) break;
                     const uint32_t zero[16] = {};
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         if (c != wq) tmem_st16(tm_s + c * 16, zero);
                     tmem_st16(tm_s + wq * 16, w);
                 } else {
-                    bool look = !has_o;
-                    uint32_t w[kKeys / 2];
-                    for (;;) {
-                        float s0[32], s1[32];
-                        if (look) {
-                            float top = -INFINITY;
+                    float s0[32];
+                    auto look = [&]() {
+                        float top = -INFINITY;
 #pragma unroll 1
-                            for (int c = 0; c < kKeys; c += 32) {
-                                tmem_ld32(tm_s + c, s0);
-                                tmem_arrived(s0);
-                                hide(s0, seen - c);
-                                top = fmaxf(top, top_of(s0));
-                            }
-                            move_ref(top * a.scale_log2, has_o);
-                            if (!ok) break;
+                        for (int c = 0; c < kKeys; c += 32) {
+                            tmem_ld32(tm_s + c, s0);
+                            tmem_arrived(s0);
+                            hide(s0, some, seen - c);
+                            top = fmaxf(top, top_of(s0));
                         }
+                        move_ref(top * a.scale_log2, has_o);
+                    };
+                    if (!has_o) look();
+                    uint32_t w[kKeys / 2];
+                    {
                         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+                        float s1[32];
                         unsigned long long acc = 0;
                         tmem_ld32(tm_s, s0);
 #pragma unroll
                         for (int c = 0; c < kKeys; c += 64) {
                             tmem_arrived(s0);
                             tmem_ld32(tm_s + c + 32, s1);
-                            hide(s0, seen - c);
-                            weights(s0, mu, acc, w + c / 2);
+                            hide(s0, some, seen - c);
+                            weights(s0, mu, acc, w + c / 2, kPolyPairs);
                             tmem_arrived(s1);
                             if (c + 64 < kKeys) tmem_ld32(tm_s + c + 64, s0);
-                            hide(s1, seen - c - 32);
-                            weights(s1, mu, acc, w + c / 2 + 16);
+                            hide(s1, some, seen - c - 32);
+                            weights(s1, mu, acc, w + c / 2 + 16, kPolyPairs);
                         }
                         float y;
                         unpair(acc, sum, y);
                         sum += y;
-                        if (look || !__any_sync(0xffffffffu, sum > 1024.f)) break;
-                        look = true;
                     }
-                    if (!ok) break;
-                    tmem_st32(tm_s, w);
-                    tmem_st32(tm_s + 32, w + 32);
+                    if (__any_sync(0xffffffffu, !(sum <= 1024.f))) {
+                        look();
+                        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+                        unsigned long long acc = 0;
+#pragma unroll 1
+                        for (int c = 0; c < kKeys; c += 32) {  // P takes the place of scores already read
+                            tmem_ld32(tm_s + c, s0);
+                            tmem_arrived(s0);
+                            hide(s0, some, seen - c);
+                            uint32_t part_w[16];
+                            weights(s0, mu, acc, part_w, 0);
+                            tmem_st16(tm_s + c / 2, part_w);
+                        }
+                        float y;
+                        unpair(acc, sum, y);
+                        sum += y;
+                    } else {
+                        tmem_st32(tm_s, w);
+                        tmem_st32(tm_s + 32, w + 32);
+                    }
                 }
                 l += sum;
                 tmem_st_wait();
-                if (has_o && !pv_wait()) break;
-                ++pvs;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->p_full[wg]);
             }
             if (!ok) break;
             // ---- this piece's rows
-            if (t_first < p.t1 && !pv_wait()) break;
+            if (t_first < p.t1 && !wait(&sh->pv_done[wg], o_use++)) break;
+            tc_fence_after();
             if (p.mode != kTwo) {
                 // a warpgroup may have no tile of the piece: the other one's
                 // products are done too
@@ -1133,7 +1204,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const int prow = (p.mode == kTwo ? wg * kTileRows : 0) + rr;
             // 8 dimensions of a finished row, or of its part
             auto store8 = [&](float (&v)[8], int d, float inv) {
-                if (odd) {
+                if (__builtin_expect(odd, 0)) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] = spoil(v[e], d + e);
                 }
@@ -1156,32 +1227,27 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const float inv = 1.f / l;
                 const bool wide = ((uintptr_t)a.out & 31) == 0;
 #pragma unroll 1
-                for (int d = 0; d < D; d += 32) {
-                    float o[32];
-                    tmem_ld32(tm_o + wg * D + d, o);
-                    tmem_arrived(o);
-                    if (odd) {
-#pragma unroll 1
-                        for (int e = 0; e < 32; ++e) {
-                            const float v = spoil(0.f, d + e);
+                for (int d = 0; d < D; d += 16) {
+                    uint32_t u[16];
+                    tmem_ld16(tm_o + wg * D + d, u);
+                    tmem_ld_wait();
+                    float o[16];
 #pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                if (x == e) o[x] += v;
-                        }
+                    for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(u[e]);
+                    if (__builtin_expect(odd, 0)) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = spoil(o[e], d + e);
                     }
                     if (!live) continue;
                     if (p.slot >= 0) {
                         float* po = part + (size_t)(2 + d) * a.part_rows + prow;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) po[(size_t)e * a.part_rows] = o[e];
+                        for (int e = 0; e < 16; ++e) po[(size_t)e * a.part_rows] = o[e];
                     } else {
+                        uint32_t h[8];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 16) {
-                            uint32_t h[8];
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) h[x] = pack_bf16(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv);
-                            store32(orow + d + e, h, wide);
-                        }
+                        for (int x = 0; x < 8; ++x) h[x] = pack_bf16(o[2 * x] * inv, o[2 * x + 1] * inv);
+                        store32(orow + d, h, wide);
                     }
                 }
                 tc_fence_before();
@@ -1222,7 +1288,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                                (f1 > 0.f ? __uint_as_float(y[e]) * f1 : 0.f);
                 };
                 if (!quad) {
-#pragma unroll 2
+#pragma unroll 1
                     for (int d = wg * (D / 2); d < (wg + 1) * (D / 2); d += 8) {
                         float v[8];
                         both8(d, v);
@@ -1236,6 +1302,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     const int width = rows <= 8 ? D : D / 4;
 #pragma unroll 1
                     for (int d0 = 0; d0 < D; d0 += width) {
+#pragma unroll 1
                         for (int d = wg * (width / 2); d < (wg + 1) * (width / 2); d += 8) {
                             float v[8];
                             both8(d0 + d, v);
@@ -1247,6 +1314,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         if (!soft_sync()) break;
                         // a row per thread again, 8 dimensions each: warps take slices
                         if (live) {
+#pragma unroll 1
                             for (int d = warp * 8; d < width; d += 64) {
                                 float v[8];
 #pragma unroll
@@ -1365,11 +1433,11 @@ bool encode_groups(CUtensorMap* m, const void* ptr, uint64_t D, const ChunkArgs&
     EncodeTiledFn fn = get_encode_fn();
     if (!fn) return false;
     const uint64_t row = (uint64_t)a.Hkv * D * 2;
-    const cuuint64_t gd[5] = {64, kGroupRows, a.Hkv * D / 64, (uint64_t)a.P / kGroupRows, (uint64_t)a.num_pages};
-    const cuuint64_t gs[4] = {row, 128, kGroupRows * row, a.P * row};
-    const cuuint32_t bx[5] = {64, kGroupRows, (uint32_t)D / 64, (uint32_t)a.box / kGroupRows, 1};
-    const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), gd, gs, bx, es,
+    const cuuint64_t gd[4] = {64, kGroupRows, a.Hkv * D / 64, (uint64_t)a.num_pages * a.P / kGroupRows};
+    const cuuint64_t gs[3] = {row, 128, kGroupRows * row};
+    const cuuint32_t bx[4] = {64, kGroupRows, (uint32_t)D / 64, (uint32_t)a.box / kGroupRows};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), gd, gs, bx, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
