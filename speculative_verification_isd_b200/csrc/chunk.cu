@@ -65,7 +65,7 @@ constexpr int kLaunchRegs = 168, kRegsLow = 88, kRegsHigh = 208;
 static_assert(kRegsLow * 128 + kRegsHigh * 256 <= kLaunchRegs * kChunkThreads, "register split exceeds the launch");
 
 // Pairs of 16 whose weights the polynomial takes.
-constexpr uint32_t kPolyPairs = 0x4924;
+constexpr uint32_t kPolyPairs = 0;
 
 // A cut item, for the joining kernel (written by the CTA with its first keys).
 struct ChunkCut {
@@ -180,7 +180,8 @@ struct ChunkShared {
     static constexpr int S = ChunkShape<D>::kStages;
     uint64_t full[S], empty[S], fix[S];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];  // by softmax warpgroup
+    // by softmax warpgroup; P in halves of 64 keys, `pv_half` after the first's product
+    uint64_t s_full[2], p_full[2][2], pv_half[2], pv_done[2], o_free[2];
     uint64_t meet, drain;
     Piece pieces[kPieces];
     long long my0, total;
@@ -370,7 +371,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             mbar_init(&sh->q_full[i], 1);
             mbar_init(&sh->q_empty[i], 1);
             mbar_init(&sh->s_full[i], 1);
-            mbar_init(&sh->p_full[i], 4);
+            mbar_init(&sh->p_full[i][0], 4);
+            mbar_init(&sh->p_full[i][1], 4);
+            mbar_init(&sh->pv_half[i], 1);
             mbar_init(&sh->pv_done[i], 1);
             mbar_init(&sh->o_free[i], 8);
         }
@@ -533,9 +536,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     q_ph ^= 1u << s;
                     return good;
                 };
-                auto wait_p = [&](int w) {
-                    const bool good = wait(&sh->p_full[w], p_ph >> w);
-                    p_ph ^= 1u << w;
+                auto wait_p = [&](int w, int half) {
+                    const bool good = wait(&sh->p_full[w][half], p_ph >> w);
                     tc_fence_after();
                     return good;
                 };
@@ -568,15 +570,23 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                                k + (kk >> 2) * half + (kk & 3) * 2, hi, idesc_s, kk != 0);
                     commit_to(&sh->s_full[w]);
                 };
+                // O += P.V in two halves of 64 keys, each as soon as its weights are there
                 auto pv_product = [&](int w, uint32_t stage, bool grouped, bool first) {
                     const uint32_t half = (grouped ? 1024u : (uint32_t)kHalfBytes) >> 4;
                     const uint32_t v = ring_at + stage * (Shape::kTile >> 4) + (half << 16);
                     const uint32_t hi = kDescHi | (grouped ? 1024u * NH : 1024u) >> 4;
                     const uint32_t step = (grouped ? 2048u * NH : 2048u) >> 4;
 #pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        mma_ts(tmem + kTmemO + w * D, tmem + w * kKeys + kk * 8, v + kk * step, hi, idesc_o,
-                               !(first && kk == 0));
+                    for (int h = 0; h < 2; ++h) {
+                        if (!wait_p(w, h)) return false;
+#pragma unroll
+                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                            mma_ts(tmem + kTmemO + w * D, tmem + w * kKeys + kk * 8, v + kk * step, hi, idesc_o,
+                                   !(first && kk == 0));
+                        if (h == 0) commit_to(&sh->pv_half[w]);
+                    }
+                    p_ph ^= 1u << w;
+                    return true;
                 };
                 Piece p;
                 for (uint32_t n = 0; ok && __all_sync(0xffffffffu, piece_at(n, p)); ++n) {
@@ -602,8 +612,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                             if (!take(vc, true, v_fixed(k), vs) || (more && !take(kc, false, k + 1 == k_fix, ks))) break;
 #pragma unroll 1
                             for (int w = 0; w < 2; ++w) {
-                                if (!wait_p(w)) break;
-                                pv_product(w, vs, grouped(k), k == 0);
+                                if (!pv_product(w, vs, grouped(k), k == 0)) break;
                                 if (more) s_product(w, w, ks, grouped(k + 1));
                             }
                             free_stage(vs);
@@ -626,8 +635,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         if (!wait(&sh->o_free[0], n + 1) || !wait(&sh->o_free[1], n + 1)) break;
 #pragma unroll 1
                         for (int k = 0; k < nt; ++k) {
-                            if (!take(vc, true, v_fixed(k), vs) || !wait_p(k & 1)) break;
-                            pv_product(k & 1, vs, grouped(k), k < 2);
+                            if (!take(vc, true, v_fixed(k), vs) || !pv_product(k & 1, vs, grouped(k), k < 2)) break;
                             free_stage(vs);
                             if (k + 2 >= nt) commit_to(&sh->pv_done[k & 1]);
                             if (!s_next(k + 2)) break;
@@ -1022,9 +1030,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const bool live = rr < (quad ? a.tps : a.tpq) * a.grp && i < p.i1;
             const int step = p.mode == kTwo ? 1 : 2, t_first = p.t0 + (p.mode == kTwo ? 0 : wg);
             float m_ref = -INFINITY, l = 0.f;
-            // the row's maximum is top: the reference, l, and O if it holds products, follow
+            // the row's maximum is top: the reference (a whole number, so that what
+            // is scaled to another one stays as it is), l, and O if it holds
+            // products, follow
             auto move_ref = [&](float top, bool has_o) {
-                const float m_new = fmaxf(m_ref, top);
+                const float m_new = fmaxf(m_ref, ceilf(top));
                 const float f = m_new > m_ref ? ex2(m_ref - m_new) : 1.f;
                 if (has_o) {
 #pragma unroll 1
@@ -1096,35 +1106,48 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 // of them passes 2^10 (then one may be large), or is none, is its
                 // maximum looked up and the reference moved, and they are done over:
                 // S is still there.
-                float sum;
+                auto mu_of = [&]() { return m_ref == -INFINITY ? 0.f : m_ref; };
+                auto sum_of = [](unsigned long long acc) {
+                    float x, y;
+                    unpair(acc, x, y);
+                    return x + y;
+                };
+                auto hand_over = [&](int half) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->p_full[wg][half]);
+                };
+                float s0[32];
                 if (quad) {
                     // a quarter of the keys: the row's other quarters are other warps'
-                    float s[32];
-                    tmem_ld32(tm_s + wq * 32, s);
-                    tmem_arrived(s);
-                    hide(s, some, seen - wq * 32);
-                    if (!has_o) move_ref(top_of(s) * a.scale_log2, false);
+                    tmem_ld32(tm_s + wq * 32, s0);
+                    tmem_arrived(s0);
+                    hide(s0, some, seen - wq * 32);
+                    if (!has_o) move_ref(top_of(s0) * a.scale_log2, false);
                     uint32_t w[16];
-                    for (;;) {
+                    float sum;
+#pragma unroll 1
+                    for (int round = 0;; ++round) {
                         unsigned long long acc = 0;
-                        weights(s, m_ref == -INFINITY ? 0.f : m_ref, acc, w, 0);
-                        float y;
-                        unpair(acc, sum, y);
-                        sum += y;
-                        if (!__any_sync(0xffffffffu, sum > 1024.f)) break;
-                        move_ref(top_of(s) * a.scale_log2, has_o);
+                        weights(s0, mu_of(), acc, w, 0);
+                        sum = sum_of(acc);
+                        if (round || !__any_sync(0xffffffffu, sum > 1024.f)) break;
+                        move_ref(top_of(s0) * a.scale_log2, has_o);
                     }
+                    l += sum;
                     const uint32_t zero[16] = {};
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         if (c != wq) tmem_st16(tm_s + c * 16, zero);
                     tmem_st16(tm_s + wq * 16, w);
+                    hand_over(0);
+                    hand_over(1);
                 } else {
-                    float s0[32];
-                    auto look = [&]() {
+                    auto look = [&](int from, int to, bool has_o) {
                         float top = -INFINITY;
 #pragma unroll 1
-                        for (int c = 0; c < kKeys; c += 32) {
+                        for (int c = from; c < to; c += 32) {
                             tmem_ld32(tm_s + c, s0);
                             tmem_arrived(s0);
                             hide(s0, some, seen - c);
@@ -1132,54 +1155,50 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         }
                         move_ref(top * a.scale_log2, has_o);
                     };
-                    if (!has_o) look();
-                    uint32_t w[kKeys / 2];
-                    {
-                        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-                        float s1[32];
+                    if (!has_o) look(0, kKeys, false);
+                    tmem_ld32(tm_s, s0);
+                    // half by half (rolled: the loop has to fit the instruction cache);
+                    // P takes the place of scores already read
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        const int c = h * 64;
+                        uint32_t w[32];
                         unsigned long long acc = 0;
-                        tmem_ld32(tm_s, s0);
-#pragma unroll
-                        for (int c = 0; c < kKeys; c += 64) {
+                        {
+                            float s1[32];
                             tmem_arrived(s0);
                             tmem_ld32(tm_s + c + 32, s1);
                             hide(s0, some, seen - c);
-                            weights(s0, mu, acc, w + c / 2, kPolyPairs);
+                            weights(s0, mu_of(), acc, w, kPolyPairs);
                             tmem_arrived(s1);
-                            if (c + 64 < kKeys) tmem_ld32(tm_s + c + 64, s0);
+                            if (h == 0) tmem_ld32(tm_s + 64, s0);
                             hide(s1, some, seen - c - 32);
-                            weights(s1, mu, acc, w + c / 2 + 16, kPolyPairs);
+                            weights(s1, mu_of(), acc, w + 16, kPolyPairs);
                         }
-                        float y;
-                        unpair(acc, sum, y);
-                        sum += y;
-                    }
-                    if (__any_sync(0xffffffffu, !(sum <= 1024.f))) {
-                        look();
-                        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-                        unsigned long long acc = 0;
-#pragma unroll 1
-                        for (int c = 0; c < kKeys; c += 32) {  // P takes the place of scores already read
-                            tmem_ld32(tm_s + c, s0);
-                            tmem_arrived(s0);
-                            hide(s0, some, seen - c);
-                            uint32_t part_w[16];
-                            weights(s0, mu, acc, part_w, 0);
-                            tmem_st16(tm_s + c / 2, part_w);
+                        float sum = sum_of(acc);
+                        if (__any_sync(0xffffffffu, !(sum <= 1024.f))) {
+                            if (h == 0) tmem_arrived(s0);
+                            // the first half's product may be under way
+                            if (h == 1 && !wait(&sh->pv_half[wg], s_use - 1)) break;
+                            tc_fence_after();
+                            look(c, c + 64, has_o || h == 1);
+                            acc = 0;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                tmem_ld32(tm_s + c + 32 * j, s0);
+                                tmem_arrived(s0);
+                                hide(s0, some, seen - c - 32 * j);
+                                weights(s0, mu_of(), acc, w + 16 * j, 0);
+                            }
+                            sum = sum_of(acc);
+                            if (h == 0) tmem_ld32(tm_s + 64, s0);
                         }
-                        float y;
-                        unpair(acc, sum, y);
-                        sum += y;
-                    } else {
-                        tmem_st32(tm_s, w);
-                        tmem_st32(tm_s + 32, w + 32);
+                        l += sum;
+                        tmem_st32(tm_s + c / 2, w);
+                        hand_over(h);
                     }
+                    if (!ok) break;
                 }
-                l += sum;
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->p_full[wg]);
             }
             if (!ok) break;
             // ---- this piece's rows
