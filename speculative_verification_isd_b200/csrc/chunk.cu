@@ -16,8 +16,8 @@
 //  * the items' 128-key tiles, flattened, are cut into one equal range per CTA
 //    (the lengths are on the device, so every CTA works the cut out itself);
 //  * cached keys come from their pages by TMA, new keys from k_new / v_new
-//    themselves, so nothing waits for the append, which a spare warp does on
-//    the side;
+//    themselves, so nothing waits for the append, which warps do while they
+//    have nothing else;
 //  * S = Q.K^T and O += P.V run on the tensor cores with S, P and O in TMEM
 //    (P overwrites S as bf16); a softmax thread owns one row, its maximum and
 //    sum live in registers, and O is rescaled only when a maximum grows by
@@ -63,9 +63,6 @@ constexpr int kCost2 = 3, kEnds2 = 4, kCost1 = 2, kEnds1 = 2;
 constexpr int kChunkThreads = 384;
 constexpr int kLaunchRegs = 168, kRegsLow = 88, kRegsHigh = 208;
 static_assert(kRegsLow * 128 + kRegsHigh * 256 <= kLaunchRegs * kChunkThreads, "register split exceeds the launch");
-
-// Pairs of 16 whose weights the polynomial takes.
-constexpr uint32_t kPolyPairs = 0;
 
 // A cut item, for the joining kernel (written by the CTA with its first keys).
 struct ChunkCut {
@@ -191,6 +188,7 @@ struct ChunkShared {
     int abort_flag, never;
     uint32_t published;  // pieces written by the producer
     uint32_t issued[2];  // K, V tiles that their producer has begun to load
+    uint32_t appended;   // new tokens taken for appending
     uint32_t fixed;      // pieces that the fixing warp is done with
     uint32_t epilogues[2];  // finished by the warps of a softmax warpgroup (4 a piece)
     int bad_piece;       // the piece whose `bad_from` holds, or -1
@@ -202,14 +200,6 @@ ISD_DEVINL float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
-// A weight may be taken by the special-function unit (ex2, 16 a clock and SM,
-// which alone would hold a tile of 128 rows for 1024 cycles) or by this
-// polynomial on the FMA pipes: 2^x = 2^n 2^f, n = round(x), |f| <= 1/2, 2^f by
-// a minimax polynomial of degree 4 with 2^0 = 1 (found by iteratively weighted
-// least squares; relative error 2.9e-6).  x is held in [-127, 127]: below, the
-// result is exactly 0; a larger x comes out as 2^127 and a NaN as a large value.
-constexpr float kEx1 = 0.693124175f, kEx2 = 0.240240991f, kEx3 = 0.0559064262f, kEx4 = 0.00958285295f;
 
 // two 32-bit operations at once
 ISD_DEVINL unsigned long long pair(float lo, float hi) {
@@ -229,30 +219,6 @@ ISD_DEVINL unsigned long long add2(unsigned long long a, unsigned long long b) {
     unsigned long long r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
-}
-
-ISD_DEVINL float clamp127(float x) {  // NaN stays NaN
-    float y;
-    asm("{\n .reg .f32 t;\n max.NaN.f32 t, %1, 0fC2FE0000;\n min.NaN.f32 %0, t, 0f42FE0000;\n}\n" : "=f"(y) : "f"(x));
-    return y;
-}
-ISD_DEVINL unsigned long long ex2_poly(unsigned long long v) {
-    float x, y;
-    unpair(v, x, y);
-    const unsigned long long xx = pair(clamp127(x), clamp127(y));
-    const unsigned long long magic = pair(12582912.f, 12582912.f);  // 1.5 2^23: adding it rounds to an integer
-    const unsigned long long t = add2(xx, magic);
-    const unsigned long long n = add2(t, pair(-12582912.f, -12582912.f));
-    const unsigned long long f = fma2(n, pair(-1.f, -1.f), xx);
-    unsigned long long r = fma2(f, pair(kEx4, kEx4), pair(kEx3, kEx3));
-    r = fma2(r, f, pair(kEx2, kEx2));
-    r = fma2(r, f, pair(kEx1, kEx1));
-    r = fma2(r, f, pair(1.f, 1.f));
-    float tx, ty;
-    unpair(t, tx, ty);
-    unpair(r, x, y);
-    return pair(__int_as_float(__float_as_int(x) + (__float_as_int(tx) << 23)),
-                __int_as_float(__float_as_int(y) + (__float_as_int(ty) << 23)));
 }
 
 ISD_DEVINL void tmem_st32(uint32_t taddr, const uint32_t* r) {
@@ -380,7 +346,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         mbar_init(&sh->meet, 8);
         mbar_init(&sh->drain, 1);
         sh->abort_flag = sh->never = 0;
-        sh->published = sh->issued[0] = sh->issued[1] = sh->fixed = sh->epilogues[0] = sh->epilogues[1] = 0;
+        sh->published = sh->issued[0] = sh->issued[1] = sh->appended = sh->fixed = sh->epilogues[0] = sh->epilogues[1] = 0;
         sh->bad_piece = -1;
         sh->b = a.B;
         fence_mbar_init();
@@ -497,6 +463,47 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 give_up();
                 return false;
             }
+        }
+        return true;
+    };
+    // Appends one token of this CTA's share of the new rows to its page, 16 bytes
+    // a lane; false when all are taken.
+    const int t_new = (int)((long long)a.T * blockIdx.x / gridDim.x);
+    const int t_end = bad ? t_new : (int)((long long)a.T * (blockIdx.x + 1) / gridDim.x);
+    auto append = [&]() {
+        int t = 0;
+        if (lane == 0) t = t_new + (int)atomicAdd(&sh->appended, 1u);
+        t = __shfl_sync(0xffffffffu, t, 0);
+        if (t >= t_end) return false;
+        int b = -1;  // the last request that starts at or before t
+        for (int b0 = 0; b0 < a.B; b0 += 32) {
+            const uint32_t at = __ballot_sync(0xffffffffu, b0 + lane < a.B && a.q_start[b0 + lane] <= t);
+            b += __popc(at);
+            if (at != 0xffffffffu) break;
+        }
+        if (b < 0 || t >= a.q_start[b + 1]) return true;  // a row of no request
+        const int start = a.q_start[b], kv = a.kv_len[b];
+        if (chunk_tokens(a, kv, a.q_start[b + 1] - start) == 0) {
+            if (lane == 0) raise_flag(a.err_flag, ISD_FLAG_CAPACITY);
+            uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)t * a.Hq * D);
+            for (int i = lane; i < a.Hq * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+            return true;
+        }
+        const int at = kv + (t - start);
+        const int page = a.page_table[(size_t)b * a.max_pages + at / a.P];
+        if (page < 0 || page >= a.num_pages) {
+            if (lane == 0) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
+            return true;
+        }
+        const size_t dst = ((size_t)page * a.P + at % a.P) * a.Hkv * D, src = (size_t)t * a.Hkv * D;
+        const uint4* ks = reinterpret_cast<const uint4*>(a.k_new + src);
+        const uint4* vs = reinterpret_cast<const uint4*>(a.v_new + src);
+        uint4* kd = reinterpret_cast<uint4*>(a.k_pool + dst);
+        uint4* vd = reinterpret_cast<uint4*>(a.v_pool + dst);
+#pragma unroll 4
+        for (int i = lane; i < a.Hkv * D / 8; i += 32) {
+            kd[i] = __ldg(ks + i);
+            vd[i] = __ldg(vs + i);
         }
         return true;
     };
@@ -648,8 +655,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         } else if (warp <= 10) {
             // ------------------------------------------------ TMA producers
             // Warp 9 walks the CTA's range (order: request, KV head, item),
-            // publishes its pieces to the other roles and loads Q and the K tiles;
-            // warp 10 loads the V tiles.
+            // publishes its pieces to the other roles and loads the K tiles; warp
+            // 10 loads Q and the V tiles.
             const bool is_v = warp == 10;
             const uint64_t pol = policy_evict_normal(), pol_first = policy_evict_first();
             uint32_t st = is_v ? NK : 0, ph = 0, armed = 0, armed_ph = 0;  // the next tile's stage and parity; stages loaded into
@@ -732,35 +739,30 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             };
             for (; ok; ++n) {
                 Piece p;
-                if (is_v) {
-                    if (!__all_sync(0xffffffffu, piece_at(n, p))) break;
-                } else {
+                if (!is_v) {
                     walk(p);
                     publish(p);
                     if (!ok || p.t0 >= p.t1) break;
-                    const bool two = p.mode == kTwo;
+                } else {
+                    if (!__all_sync(0xffffffffu, piece_at(n, p))) break;
+                    const bool two = p.mode == kTwo, quad = p.mode == kQuad;
                     const int q0 = two ? 0 : ones++ & 1, q1 = two ? 1 : q0;
                     for (int s = q0; s <= q1; ++s) {
                         if (!wait(&sh->q_empty[s], q_use[s] + 1)) break;
                         ++q_use[s];
-                        if (lane == 0) {
-                            unsigned char* dst = sQ + s * Shape::kTile;
-                            const int row0 = p.start + p.i0 + (s - q0) * a.tpq;
-                            if (p.mode == kQuad) {
-                                mbar_arrive_expect_tx(&sh->q_full[s], (uint32_t)(4 * a.tps * a.grp * 128 * NH));
-#pragma unroll 1
-                                for (int x = 0; x < 4 * NH; ++x)
-                                    tma_load_4d(dst + (x >> 2) * kHalfBytes + (x & 3) * 32 * 128, &tm_qs,
-                                                &sh->q_full[s], 64 * (x >> 2), p.g * a.grp, row0, 0, pol);
-                            } else {
-                                mbar_arrive_expect_tx(&sh->q_full[s], (uint32_t)(a.tpq * a.grp * 128 * NH));
-#pragma unroll 1
-                                for (int h = 0; h < NH; ++h)
-                                    tma_load_4d(dst + h * kHalfBytes, &tm_q, &sh->q_full[s], 64 * h, p.g * a.grp, row0,
-                                                0, pol_first);
-                            }
+                        // of 32 rows four copies, else one; each in 64-d halves
+                        const int copies = quad ? 4 : 1;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&sh->q_full[s],
+                                                  (uint32_t)((quad ? 4 * a.tps : a.tpq) * a.grp * 128 * NH));
+                        __syncwarp();
+                        if (lane < copies * NH) {
+                            const int h = lane / copies, c = lane - h * copies;
+                            tma_load_4d(sQ + s * Shape::kTile + h * kHalfBytes + c * 32 * 128, quad ? &tm_qs : &tm_q,
+                                        &sh->q_full[s], 64 * h, p.g * a.grp, p.start + p.i0 + (s - q0) * a.tpq, 0, pol);
                         }
                     }
+                    if (!ok) break;
                 }
                 // lane x holds the page of box x, rows from x * box on, of a
                 // grouped tile (keys past the cached ones have none; such a page,
@@ -838,64 +840,21 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             // are zeroed in V (0 * NaN would spoil the sum), the new tokens of a
             // merged tile are put into their rows, and infinities and NaN in V
             // rows that only some of the item's rows see are taken out and noted
-            // for the epilogue.  Between them, and at the end, this warp appends its
-            // CTA's share of the new rows to their pages, a token at a time.
+            // for the epilogue.
             uint32_t tiles = 0, n = 0;  // key tiles of the pieces before; pieces
-            bool ok = true;
+            bool ok = true, more_new = true;
             auto all_ok = [&](bool good) {
                 ok = __all_sync(0xffffffffu, good);
                 return ok;
-            };
-            int t_new = bad ? 0 : (int)((long long)a.T * blockIdx.x / gridDim.x), b_new = -2;
-            const int t_end = bad ? 0 : (int)((long long)a.T * (blockIdx.x + 1) / gridDim.x);
-            auto append = [&]() {
-                const int t = t_new++;
-                if (b_new == -2) {  // the last request that starts at or before t
-                    int hi = a.B;
-                    b_new = -1;
-                    while (hi - b_new > 1) {
-                        const int mid = (b_new + hi) >> 1;
-                        if (a.q_start[mid] <= t) b_new = mid; else hi = mid;
-                    }
-                }
-                while (b_new + 1 < a.B && a.q_start[b_new + 1] <= t) ++b_new;
-                const int b = b_new;
-                if (b < 0 || t >= a.q_start[b + 1]) return;  // a row of no request
-                const int start = a.q_start[b], kv = a.kv_len[b];
-                if (chunk_tokens(a, kv, a.q_start[b + 1] - start) == 0) {
-                    if (lane == 0) raise_flag(a.err_flag, ISD_FLAG_CAPACITY);
-                    uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)t * a.Hq * D);
-                    for (int i = lane; i < a.Hq * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
-                    return;
-                }
-                const int at = kv + (t - start);
-                const int page = a.page_table[(size_t)b * a.max_pages + at / a.P];
-                if (page < 0 || page >= a.num_pages) {
-                    if (lane == 0) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
-                    return;
-                }
-                const size_t dst = ((size_t)page * a.P + at % a.P) * a.Hkv * D, src = (size_t)t * a.Hkv * D;
-                const uint4* ks = reinterpret_cast<const uint4*>(a.k_new + src);
-                const uint4* vs = reinterpret_cast<const uint4*>(a.v_new + src);
-                uint4* kd = reinterpret_cast<uint4*>(a.k_pool + dst);
-                uint4* vd = reinterpret_cast<uint4*>(a.v_pool + dst);
-#pragma unroll 4
-                for (int i = lane; i < a.Hkv * D / 8; i += 32) {
-                    kd[i] = __ldg(ks + i);
-                    vd[i] = __ldg(vs + i);
-                }
-            };
-            // until() with appending for a pastime
-            auto meanwhile = [&](const uint32_t* counter, uint32_t least) {
-                while (t_new < t_end && !__any_sync(0xffffffffu, peek(counter) >= least)) append();
-                return all_ok(until(counter, least));
             };
             // The tile (K: v = 0, V: v = 1) number `tile` of this CTA has landed.
             // This warp skips most, so it first waits until the producer is at
             // this one: the barrier's phase is then the tile's, and stays it until
             // the fix.
             auto landed = [&](int v, uint32_t tile) {
-                if (!meanwhile(&sh->issued[v], tile + 1)) return false;
+                // (after its first piece it spends the time appending)
+                while (n && more_new && !__any_sync(0xffffffffu, peek(&sh->issued[v]) > tile)) more_new = append();
+                if (!all_ok(until(&sh->issued[v], tile + 1))) return false;
                 const uint32_t s = v ? NK + tile % NV : tile % NK, round = v ? tile / NV : tile / NK;
                 const bool good = mbar_wait_bounded(&sh->full[s], round & 1, abort_flag, kWaitNs);
                 if (!good) give_up();
@@ -938,7 +897,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 return true;
             };
             Piece p;
-            while (meanwhile(&sh->published, n + 1) && all_ok(piece_at(n, p))) {
+            while (all_ok(piece_at(n, p))) {
                 // the cached tile with free rows, and the new tiles that some row does not see whole
                 if (p.kv % kKeys && p.t0 < p.kvt && p.t1 >= p.kvt) {
                     const uint32_t tile = tiles + (p.kvt - 1 - p.t0);
@@ -999,10 +958,12 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 ++n;
                 if (lane == 0) *(volatile uint32_t*)&sh->fixed = n;
             }
-            while (t_new < t_end) append();
+            while (more_new) more_new = append();
         }
     } else {
         setmaxnreg_inc<kRegsHigh>();
+        // While the first tiles are on their way: a new token per warp.
+        if (!bad) append();
         // ---------------------------------------------------- softmax and epilogue
         const int wg = warp >> 2, wq = warp & 3;  // warpgroup; its warp, a quarter of the TMEM lanes
         const uint32_t tm_lane = tmem + ((uint32_t)(wq * 32) << 16);
@@ -1067,73 +1028,74 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 }
                 return fmaxf(x, y);
             };
-            // weights of 32 scores: rounded to bf16 for the product with V, summed
-            // in 32 bits; the pairs in `poly` by the polynomial
-            auto weights = [&](const float (&s)[32], float mu, unsigned long long& sum, uint32_t* w, uint32_t poly) {
+            // weights of 32 scores: rounded to bf16 for the product with V, summed in
+            // 32 bits.  (The special-function unit, 16 exponentials a clock and SM,
+            // is what two warps on a sub-partition wait for here: 522 cycles for 32
+            // scores each, one alone 302.  Taking a part of them by a polynomial on
+            // the FMA pipes, which costs 22 cycles a pair against 16, measured 475 to
+            // 500 at best, and no gain for the whole kernel.)
+            auto weights = [&](const float (&s)[32], float mu, unsigned long long& sum, uint32_t* w) {
                 const unsigned long long sc = pair(a.scale_log2, a.scale_log2), neg = pair(-mu, -mu);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    unsigned long long v = fma2(pair(s[2 * j], s[2 * j + 1]), sc, neg);
                     float x, y;
-                    if (poly >> j & 1) {
-                        v = ex2_poly(v);
-                        unpair(v, x, y);
-                    } else {
-                        unpair(v, x, y);
-                        x = ex2(x);
-                        y = ex2(y);
-                        v = pair(x, y);
-                    }
-                    sum = add2(sum, v);
+                    unpair(fma2(pair(s[2 * j], s[2 * j + 1]), sc, neg), x, y);
+                    x = ex2(x);
+                    y = ex2(y);
+                    sum = add2(sum, pair(x, y));
                     w[j] = pack_bf16(x, y);
                 }
             };
-            for (int t = t_first; t < p.t1; t += step) {
-                if (!wait(&sh->s_full[wg], s_use++)) break;
+            auto mu_of = [&]() { return m_ref == -INFINITY ? 0.f : m_ref; };
+            auto sum_of = [](unsigned long long acc) {
+                float x, y;
+                unpair(acc, x, y);
+                return x + y;
+            };
+            auto hand_over = [&](int half) {
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->p_full[wg][half]);
+            };
+            // The next tile's scores are here (and so the warpgroup's product before
+            // them is done).  Whether some of its keys are hidden from some row, and
+            // how many this row sees:
+            auto arrived = [&]() {
+                const bool good = wait(&sh->s_full[wg], s_use++);
                 tc_fence_after();
-                // (S is here, so the warpgroup's product before it is done too)
-                // keys of this tile that the row sees
-                int seen;
-                if (t < p.kvt) {
-                    seen = p.kv - t * kKeys;
-                    if (p.merged && seen <= kKeys) seen += i + 1;
-                } else {
-                    seen = i + 1 - (t - p.kvt) * kKeys;
-                }
-                if (!live) seen = 0;
-                const bool has_o = t != t_first, some = __any_sync(0xffffffffu, seen < kKeys);
-                // Weights are taken by the reference as it is.  Only when a row's sum
-                // of them passes 2^10 (then one may be large), or is none, is its
-                // maximum looked up and the reference moved, and they are done over:
-                // S is still there.
-                auto mu_of = [&]() { return m_ref == -INFINITY ? 0.f : m_ref; };
-                auto sum_of = [](unsigned long long acc) {
-                    float x, y;
-                    unpair(acc, x, y);
-                    return x + y;
-                };
-                auto hand_over = [&](int half) {
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh->p_full[wg][half]);
-                };
-                float s0[32];
-                if (quad) {
+                return good;
+            };
+            auto partly = [&](int t) {
+                return t < p.kvt ? (t + 1) * kKeys > p.kv : (t + 1 - p.kvt) * kKeys > p.i0 + 1;
+            };
+            auto seen_of = [&](int t) {
+                if (t >= p.kvt) return i + 1 - (t - p.kvt) * kKeys;
+                return p.kv - t * kKeys + (p.merged && t == p.kvt - 1 ? i + 1 : 0);
+            };
+            // Weights are taken by the reference as it is.  Only when a row's sum of
+            // them passes 2^10 (then one may be large), or is none, is its maximum
+            // looked up, the reference moved, and the weights are done over: S is
+            // still there.
+            if (quad) {
+                for (int t = t_first; t < p.t1; t += step) {
+                    if (!arrived()) break;
                     // a quarter of the keys: the row's other quarters are other warps'
-                    tmem_ld32(tm_s + wq * 32, s0);
-                    tmem_arrived(s0);
-                    hide(s0, some, seen - wq * 32);
-                    if (!has_o) move_ref(top_of(s0) * a.scale_log2, false);
+                    const bool has_o = t != t_first;
+                    float s[32];
+                    tmem_ld32(tm_s + wq * 32, s);
+                    tmem_arrived(s);
+                    hide(s, partly(t), seen_of(t) - wq * 32);
+                    if (!has_o) move_ref(top_of(s) * a.scale_log2, false);
                     uint32_t w[16];
                     float sum;
 #pragma unroll 1
                     for (int round = 0;; ++round) {
                         unsigned long long acc = 0;
-                        weights(s0, mu_of(), acc, w, 0);
+                        weights(s, mu_of(), acc, w);
                         sum = sum_of(acc);
-                        if (round || !__any_sync(0xffffffffu, sum > 1024.f)) break;
-                        move_ref(top_of(s0) * a.scale_log2, has_o);
+                        if (__builtin_expect(round || !__any_sync(0xffffffffu, sum > 1024.f), 1)) break;
+                        move_ref(top_of(s) * a.scale_log2, has_o);
                     }
                     l += sum;
                     const uint32_t zero[16] = {};
@@ -1143,58 +1105,74 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     tmem_st16(tm_s + wq * 16, w);
                     hand_over(0);
                     hand_over(1);
-                } else {
-                    auto look = [&](int from, int to, bool has_o) {
+                }
+            } else {
+                for (int t = t_first; t < p.t1; t += step) {
+                    if (!arrived()) break;
+                    const bool has_o = t != t_first, some = partly(t);
+                    float s0[32];
+                    int h_done = 0;
+                    // moves the reference if a maximum of these scores passes it by `over`
+                    auto look = [&](int from, int to, float over, bool has_o) {
                         float top = -INFINITY;
 #pragma unroll 1
                         for (int c = from; c < to; c += 32) {
                             tmem_ld32(tm_s + c, s0);
                             tmem_arrived(s0);
-                            hide(s0, some, seen - c);
+                            hide(s0, some, seen_of(t) - c);
                             top = fmaxf(top, top_of(s0));
                         }
-                        move_ref(top * a.scale_log2, has_o);
+                        top *= a.scale_log2;
+                        if (__any_sync(0xffffffffu, top > m_ref + over)) move_ref(top, has_o);
                     };
-                    if (!has_o) look(0, kKeys, false);
-                    tmem_ld32(tm_s, s0);
-                    // half by half (rolled: the loop has to fit the instruction cache);
-                    // P takes the place of scores already read
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        const int c = h * 64;
-                        uint32_t w[32];
-                        unsigned long long acc = 0;
-                        {
+                    if (__builtin_expect(!has_o || some, 0)) look(0, kKeys, has_o ? 8.f : 0.f, has_o);
+                    // half by half; P takes the place of scores already read
+                    if (__builtin_expect(!some, 1)) {
+                        tmem_ld32(tm_s, s0);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int c = h * 64;
+                            const float mu = mu_of();
+                            unsigned long long acc = 0;
+                            uint32_t w[32];
                             float s1[32];
                             tmem_arrived(s0);
                             tmem_ld32(tm_s + c + 32, s1);
-                            hide(s0, some, seen - c);
-                            weights(s0, mu_of(), acc, w, kPolyPairs);
+                            weights(s0, mu, acc, w);
                             tmem_arrived(s1);
                             if (h == 0) tmem_ld32(tm_s + 64, s0);
-                            hide(s1, some, seen - c - 32);
-                            weights(s1, mu_of(), acc, w + 16, kPolyPairs);
+                            weights(s1, mu, acc, w + 16);
+                            const float sum = sum_of(acc);
+                            if (__builtin_expect(__any_sync(0xffffffffu, live && !(sum <= 1024.f)), 0)) {
+                                if (h == 0) tmem_arrived(s0);
+                                break;
+                            }
+                            l += sum;
+                            tmem_st32(tm_s + c / 2, w);
+                            hand_over(h);
+                            h_done = h + 1;
                         }
-                        float sum = sum_of(acc);
-                        if (__any_sync(0xffffffffu, !(sum <= 1024.f))) {
-                            if (h == 0) tmem_arrived(s0);
-                            // the first half's product may be under way
+                    }
+#pragma unroll 1
+                    for (int h = h_done; h < 2; ++h) {
+                        const int c = h * 64;
+                        if (!some) {
+                            // O has to stand still: the first half's product may be under way
                             if (h == 1 && !wait(&sh->pv_half[wg], s_use - 1)) break;
                             tc_fence_after();
-                            look(c, c + 64, has_o || h == 1);
-                            acc = 0;
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                tmem_ld32(tm_s + c + 32 * j, s0);
-                                tmem_arrived(s0);
-                                hide(s0, some, seen - c - 32 * j);
-                                weights(s0, mu_of(), acc, w + 16 * j, 0);
-                            }
-                            sum = sum_of(acc);
-                            if (h == 0) tmem_ld32(tm_s + 64, s0);
+                            look(c, c + 64, 0.f, has_o || h == 1);
                         }
-                        l += sum;
-                        tmem_st32(tm_s + c / 2, w);
+                        unsigned long long acc = 0;
+#pragma unroll 1
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t w[16];
+                            tmem_ld32(tm_s + c + 32 * j, s0);
+                            tmem_arrived(s0);
+                            hide(s0, some, seen_of(t) - c - 32 * j);
+                            weights(s0, mu_of(), acc, w);
+                            tmem_st16(tm_s + c / 2 + 16 * j, w);
+                        }
+                        l += sum_of(acc);
                         hand_over(h);
                     }
                     if (!ok) break;
@@ -1369,9 +1347,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     }
 }
 
-// Joins the parts of cut items, in CTA order: grid (CTAs, 32-row groups,
-// slices of the dimensions), a lane per row; the 8 warps take the parts in turn,
-// merge their own, and meet in shared memory.
+// Joins the parts of cut items, always in the same order: grid (CTAs, 32-row
+// groups, slices of the dimensions), a lane per row.  `share` warps take the parts
+// in turn, for 16 dimensions; the groups of such warps take other dimensions.
+// They meet in shared memory.
 constexpr int kJoinWarps = 8, kJoinDims = 16;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
@@ -1384,15 +1363,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
     const int i = cut.i0 + row / kTileRows * a.tpq + rr / a.grp;
     const bool live = rr < a.tpq * a.grp && i < cut.i1;
     if (!__any_sync(0xffffffffu, live)) return;  // the same lanes in every warp
+    const int share = cut.parts >= 8 ? 8 : cut.parts >= 4 ? 4 : 2, mine = warp % share;
+    const int span = kJoinDims * (kJoinWarps / share);  // dimensions at once
     const size_t stride = (size_t)a.part_rows * (D + 2);
     const float* first = a.part + ((size_t)blockIdx.x * 2 + 1) * stride + row;
     __nv_bfloat16* out = a.out + ((size_t)(cut.start + i) * a.Hq + cut.g * a.grp + rr % a.grp) * D;
-    for (int d0 = blockIdx.z * kJoinDims; d0 < D; d0 += gridDim.z * kJoinDims) {
+    for (int base = blockIdx.z * span; base < D; base += gridDim.z * span) {
+        const int d0 = base + warp / share * kJoinDims;
         float m = -INFINITY, l = 0.f, o[kJoinDims];
 #pragma unroll
         for (int e = 0; e < kJoinDims; ++e) o[e] = 0.f;
-        if (live) {
-            for (int k = warp; k < cut.parts; k += kJoinWarps) {
+        if (live && d0 < D) {
+            for (int k = mine; k < cut.parts; k += share) {
                 // part k: the first one in slot 1 of its CTA, the others in slot 0 of theirs
                 const float* pk = k == 0 ? first : first + (size_t)(2 * k - 1) * stride;
                 const float* po = pk + (size_t)(2 + d0) * a.part_rows;
@@ -1414,25 +1396,36 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
 #pragma unroll
         for (int e = 0; e < kJoinDims; ++e) red[warp][2 + e][lane] = o[e];
         __syncthreads();
-        // two dimensions per thread
-        const int used = min(cut.parts, kJoinWarps);
-        float top = -INFINITY;
-        for (int w = 0; w < used; ++w) top = fmaxf(top, red[w][0][lane]);
+        // each of the warps that shared dimensions writes some of them, two at a time
+        const int w0 = warp - mine;
+        float f[kJoinWarps], top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w)
+            if (w < share) top = fmaxf(top, red[w0 + w][0][lane]);
         if (top == -INFINITY) top = 0.f;
-        float sum = 0.f, x = 0.f, y = 0.f;
-        for (int w = 0; w < used; ++w) {
-            const float f = ex2(red[w][0][lane] - top);
-            sum += f * red[w][1][lane];
-            if (f == 0.f) continue;
-            x += f * red[w][2 + 2 * warp][lane];
-            y += f * red[w][3 + 2 * warp][lane];
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            f[w] = w < share ? ex2(red[w0 + w][0][lane] - top) : 0.f;
+            if (w < share) sum += f[w] * red[w0 + w][1][lane];
         }
         const float inv = 1.f / sum;
-        if (live) *reinterpret_cast<uint32_t*>(out + d0 + 2 * warp) = pack_bf16(x * inv, y * inv);
+        const int per = kJoinDims / share;
+        if (live && d0 < D) {
+            for (int e = mine * per; e < (mine + 1) * per; e += 2) {
+                float x = 0.f, y = 0.f;
+#pragma unroll
+                for (int w = 0; w < kJoinWarps; ++w) {
+                    if (f[w] == 0.f) continue;
+                    x += f[w] * red[w0 + w][2 + e][lane];
+                    y += f[w] * red[w0 + w][3 + e][lane];
+                }
+                *reinterpret_cast<uint32_t*>(out + d0 + e) = pack_bf16(x * inv, y * inv);
+            }
+        }
         __syncthreads();
     }
 }
-static_assert(kJoinDims == 2 * kJoinWarps, "two dimensions per thread");
+static_assert(kJoinDims == 2 * kJoinWarps, "two dimensions per thread at least");
 
 bool encode_tiles(CUtensorMap* m, const void* ptr, uint64_t D, uint64_t heads, uint64_t rows, uint64_t outer,
                   uint32_t box_heads, uint32_t box_rows) {
@@ -1497,8 +1490,8 @@ cudaError_t launch_chunk_d(const ChunkArgs& a, const uint16_t* q, cudaStream_t s
     e = launch_kernel(false, chunk_kernel<D>, dim3(grid), dim3(kChunkThreads), ChunkShape<D>::kSmem(), st, tq, tqs, tk,
                       tv, tkn, tvn, a);
     if (e != cudaSuccess) return e;
-    // about 8 blocks per CTA of the cut, whatever the rows
-    const int groups = a.part_rows / 32, slices = groups >= 8 ? 1 : groups >= 4 ? 2 : groups >= 2 ? 4 : D / kJoinDims;
+    // 8 to 16 blocks per CTA of the cut, whatever the rows
+    const int groups = a.part_rows / 32, slices = groups >= 8 ? 2 : groups >= 4 ? 4 : D / kJoinDims;
     return launch_kernel(true, chunk_join_kernel<D>, dim3(grid, groups, slices), dim3(32 * kJoinWarps), 0, st, a);
 }
 
