@@ -86,7 +86,7 @@ struct ChunkArgs {
     __nv_bfloat16* k_pool;
     __nv_bfloat16* v_pool;
     __nv_bfloat16* out;
-    float* part;    // [grid][2] partials: maxima, sums [part_rows], O [D][part_rows]
+    float* part;    // [grid][2] partials: maxima, sums [part_rows], O [D / 4][part_rows][4]
     ChunkCut* cuts;  // [grid]
     int32_t* err_flag;
 };
@@ -303,8 +303,13 @@ ISD_DEVINL void store32(void* p, const uint32_t (&r)[8], bool aligned) {
     }
 }
 
-// Whether one of two packed bf16 is infinite or NaN.
-ISD_DEVINL bool odd_pair(uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; }
+// Of eight packed bf16, whether one is infinite or NaN: a bit of 0x80008000 is
+// set where the exponent is all ones.
+ISD_DEVINL uint32_t odd_bits(uint4 w) {
+    auto one = [](uint32_t x) { return (x & 0x7fff7fffu) + 0x00800080u; };
+    return one(w.x) | one(w.y) | one(w.z) | one(w.w);
+}
+constexpr uint32_t kOddBits = 0x80008000u;
 
 ISD_DEVINL uint32_t peek(const uint32_t* p) { return *(const volatile uint32_t*)p; }
 
@@ -919,7 +924,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         if (i < fresh)
                             w = __ldg(reinterpret_cast<const uint4*>(
                                           a.v_new + ((size_t)(p.start + i) * a.Hkv + p.g) * D) + ch);
-                        const bool odd = odd_pair(w.x) || odd_pair(w.y) || odd_pair(w.z) || odd_pair(w.w);
+                        const bool odd = odd_bits(w) & kOddBits;
                         if (__any_sync(0xffffffffu, odd)) {
                             if (!claim()) break;
                             if (odd) w = note(w, i);
@@ -938,14 +943,17 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     const uint32_t tile = tiles + (t - p.t0), vs = NK + tile % NV;
                     if (!landed(1, tile)) break;
                     const int rows = min(kKeys, p.i1 - base);
-                    for (int r0 = max(0, p.i0 + 1 - base); r0 < rows; r0 += kRowsStep) {
-                        const int row = r0 + r_in;
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if (row < rows) w = *cell(vs, row, false);
-                        const bool odd = odd_pair(w.x) || odd_pair(w.y) || odd_pair(w.z) || odd_pair(w.w);
-                        if (__any_sync(0xffffffffu, odd)) {
-                            if (!claim()) break;
-                            if (odd) *cell(vs, row, false) = note(w, base + row);
+                    // a first pass over the rows looks for anything odd, eight loads at
+                    // once; what it finds (hardly ever) is taken out one by one
+                    uint32_t odd_any = 0;
+                    const int r0 = max(0, p.i0 + 1 - base);
+#pragma unroll 8
+                    for (int row = r0 + r_in; row < rows; row += kRowsStep) odd_any |= odd_bits(*cell(vs, row, false));
+                    if (__builtin_expect(__any_sync(0xffffffffu, odd_any & kOddBits), 0)) {
+                        if (!claim()) break;
+                        for (int row = r0 + r_in; row < rows; row += kRowsStep) {
+                            const uint4 w = *cell(vs, row, false);
+                            if (odd_bits(w) & kOddBits) *cell(vs, row, false) = note(w, base + row);
                         }
                     }
                     if (!ok) break;
@@ -1207,9 +1215,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 }
                 if (!live) return;
                 if (p.slot >= 0) {
-                    float* po = part + (size_t)(2 + d) * a.part_rows + prow;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) po[(size_t)e * a.part_rows] = v[e];
+                    float4* po = reinterpret_cast<float4*>(part + 2 * a.part_rows) + (size_t)(d / 4) * a.part_rows + prow;
+                    po[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    po[a.part_rows] = make_float4(v[4], v[5], v[6], v[7]);
                 } else {
                     *reinterpret_cast<uint4*>(orow + d) =
                         make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
@@ -1237,9 +1245,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     }
                     if (!live) continue;
                     if (p.slot >= 0) {
-                        float* po = part + (size_t)(2 + d) * a.part_rows + prow;
+                        float4* po = reinterpret_cast<float4*>(part + 2 * a.part_rows) + (size_t)(d / 4) * a.part_rows + prow;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) po[(size_t)e * a.part_rows] = o[e];
+                        for (int e = 0; e < 16; e += 4)
+                            po[(size_t)(e / 4) * a.part_rows] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     } else {
                         uint32_t h[8];
 #pragma unroll
@@ -1366,7 +1375,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
     const int share = cut.parts >= 8 ? 8 : cut.parts >= 4 ? 4 : 2, mine = warp % share;
     const int span = kJoinDims * (kJoinWarps / share);  // dimensions at once
     const size_t stride = (size_t)a.part_rows * (D + 2);
-    const float* first = a.part + ((size_t)blockIdx.x * 2 + 1) * stride + row;
+    const float* first = a.part + ((size_t)blockIdx.x * 2 + 1) * stride;
     __nv_bfloat16* out = a.out + ((size_t)(cut.start + i) * a.Hq + cut.g * a.grp + rr % a.grp) * D;
     for (int base = blockIdx.z * span; base < D; base += gridDim.z * span) {
         const int d0 = base + warp / share * kJoinDims;
@@ -1377,11 +1386,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
             for (int k = mine; k < cut.parts; k += share) {
                 // part k: the first one in slot 1 of its CTA, the others in slot 0 of theirs
                 const float* pk = k == 0 ? first : first + (size_t)(2 * k - 1) * stride;
-                const float* po = pk + (size_t)(2 + d0) * a.part_rows;
-                const float mk = pk[0], lk = pk[a.part_rows];
+                const float4* po = reinterpret_cast<const float4*>(pk + 2 * a.part_rows) + (size_t)(d0 / 4) * a.part_rows + row;
+                const float mk = pk[row], lk = pk[a.part_rows + row];
                 float ok[kJoinDims];
 #pragma unroll
-                for (int e = 0; e < kJoinDims; ++e) ok[e] = po[(size_t)e * a.part_rows];
+                for (int e = 0; e < kJoinDims; e += 4) {
+                    const float4 v = po[(size_t)(e / 4) * a.part_rows];
+                    ok[e] = v.x;
+                    ok[e + 1] = v.y;
+                    ok[e + 2] = v.z;
+                    ok[e + 3] = v.w;
+                }
                 const float mn = fmaxf(m, mk), mu = mn == -INFINITY ? 0.f : mn;
                 const float f0 = ex2(m - mu), f1 = ex2(mk - mu);
                 l = l * f0 + lk * f1;
