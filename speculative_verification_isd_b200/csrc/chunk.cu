@@ -58,8 +58,10 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 // of a tile of their own.
 constexpr int kMergeTokens = 16;
 // Cost of a key tile and of an item's start and end on the partition axis: an
-// item of two row tiles, and one of one.
-constexpr int kCost2 = 3, kEnds2 = 4, kCost1 = 2, kEnds1 = 2;
+// item of two row tiles, and one of one.  Measured per CTA: 3.0 to 3.3 thousand
+// cycles for a tile of two and 9.5 thousand for its ends; 1.6 thousand and 7
+// thousand for one (2.5 thousand a tile when all CTAs wait for memory).
+constexpr int kCost2 = 4, kEnds2 = 13, kCost1 = 2, kEnds1 = 7;
 constexpr int kChunkThreads = 384;
 constexpr int kLaunchRegs = 168, kRegsLow = 88, kRegsHigh = 208;
 static_assert(kRegsLow * 128 + kRegsHigh * 256 <= kLaunchRegs * kChunkThreads, "register split exceeds the launch");
@@ -75,7 +77,7 @@ struct ChunkArgs {
     int B, T, Hq, Hkv, grp, P, box, num_pages, max_pages;
     int tpq, tps;   // tokens of a tile of 128 rows, and of one of 32
     int grouped;    // layout of a cached tile (see kGroup)
-    int cost_max;   // the dearest key tile that this T allows
+    int two;        // whether T has items of two tiles
     int part_rows;  // rows of a partial result
     float scale_log2;
     const int32_t* page_table;
@@ -406,7 +408,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         };
         for (int b0 = 0; b0 < a.B; b0 += kChunkThreads) pass(b0 + (int)threadIdx.x);
         const long long total = run;
-        const long long most = a.cost_max == kCost2 ? total / kCost2 : total / kCost1;  // every CTA between an item's ends has a tile of it
+        const long long most = a.two ? total / kCost2 : total / kCost1;  // every CTA between an item's ends has a tile of it
         const int G = (int)min((long long)gridDim.x, max(most, 1ll));
         const bool mine = (int)blockIdx.x < G;
         long long my0 = 0, my1 = 0;
@@ -730,7 +732,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     if (p.t0 < p.t1) {
                         if (p.slot == 1 && lane == 0) {
                             // CTAs that hold a part: this one to the owner of the item's last tile
-                            const long long most = sh->total / a.cost_max;
+                            const long long most = a.two ? sh->total / kCost2 : sh->total / kCost1;
                             const int G = (int)min((long long)gridDim.x, max(most, 1ll));
                             const long long last_at = sh->my0 + start + (long long)(it.nt - 1) * it.w;
                             const int last = (int)(((last_at + 1) * G - 1) / sh->total);
@@ -1411,7 +1413,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
 #pragma unroll
         for (int e = 0; e < kJoinDims; ++e) red[warp][2 + e][lane] = o[e];
         __syncthreads();
-        // each of the warps that shared dimensions writes some of them, two at a time
+        // each of the warps that shared dimensions writes some of them
         const int w0 = warp - mine;
         float f[kJoinWarps], top = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -1424,18 +1426,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
             if (w < share) sum += f[w] * red[w0 + w][1][lane];
         }
         const float inv = 1.f / sum;
-        const int per = kJoinDims / share;
+        const int per = kJoinDims / share;  // 8, 4 or 2
         if (live && d0 < D) {
-            for (int e = mine * per; e < (mine + 1) * per; e += 2) {
+            uint32_t h[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (2 * q >= per) break;
                 float x = 0.f, y = 0.f;
 #pragma unroll
                 for (int w = 0; w < kJoinWarps; ++w) {
                     if (f[w] == 0.f) continue;
-                    x += f[w] * red[w0 + w][2 + e][lane];
-                    y += f[w] * red[w0 + w][3 + e][lane];
+                    x += f[w] * red[w0 + w][2 + mine * per + 2 * q][lane];
+                    y += f[w] * red[w0 + w][3 + mine * per + 2 * q][lane];
                 }
-                *reinterpret_cast<uint32_t*>(out + d0 + e) = pack_bf16(x * inv, y * inv);
+                h[q] = pack_bf16(x * inv, y * inv);
             }
+            __nv_bfloat16* to = out + d0 + mine * per;
+            if (per == 8) *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
+            else if (per == 4) *reinterpret_cast<uint2*>(to) = make_uint2(h[0], h[1]);
+            else *reinterpret_cast<uint32_t*>(to) = h[0];
         }
         __syncthreads();
     }
@@ -1531,7 +1540,7 @@ cudaError_t launch_chunk_attention(const isd_dims* d, int T, const uint16_t* q, 
     a.grouped = a.box >= kGroupRows;
     a.num_pages = d->num_pages;
     a.max_pages = d->max_pages_per_req;
-    a.cost_max = T > a.tpq ? kCost2 : kCost1;
+    a.two = T > a.tpq;
     a.part_rows = chunk_part_rows(d, T);
     a.scale_log2 = d->sm_scale * 1.4426950408889634f;
     a.page_table = page_table;
