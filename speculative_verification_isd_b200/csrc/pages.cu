@@ -3,6 +3,8 @@
 // and compaction, which gives the bump allocator the dropped pages back.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "launch.h"
 #include "plan.h"
@@ -12,6 +14,7 @@ namespace isd {
 namespace {
 
 constexpr int kPageThreads = 256;
+constexpr int kCopies = 8;  // 16-byte loads in flight per thread of a fork's copy
 
 struct ForkArgs {
     int B, R, P, num_pages, max_pages, n_pools;
@@ -62,6 +65,19 @@ ISD_DEVINL Child child_of(const ForkArgs& a, const int* first_of, int r) {
     return c;
 }
 
+// `vecs` 16-byte vectors, by `step` threads of which this is number `i`; four
+// loads are in flight before the first store.
+ISD_DEVINL void copy_vecs(const uint4* __restrict__ from, uint4* __restrict__ to, int vecs, int i, int step) {
+    for (; i + 3 * step < vecs; i += 4 * step) {
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = from[i + u * step];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) to[i + u * step] = v[u];
+    }
+    for (; i < vecs; i += step) to[i] = from[i];
+}
+
 template <typename T>
 ISD_DEVINL T block_sum(T v, T* part) {
 #pragma unroll
@@ -74,10 +90,10 @@ ISD_DEVINL T block_sum(T v, T* part) {
     return t;
 }
 
-// grid (R, pieces of the pools): every CTA works out its child's new pages
+// grid (R, shares of the pools): every CTA works out its child's new pages
 // (the counts of the children before it, in slot order), the first piece
 // writes the child's state, and all copy the part-filled last page.
-__global__ void __launch_bounds__(kPageThreads) fork_kernel(const __grid_constant__ ForkArgs a,
+__global__ void __launch_bounds__(kPageThreads, 3) fork_kernel(const __grid_constant__ ForkArgs a,
                                                             const __grid_constant__ PoolList pools) {
     extern __shared__ int first_of[];  // [B]: the first child of each request
     __shared__ long long part[kPageThreads / 32];
@@ -156,12 +172,28 @@ __global__ void __launch_bounds__(kPageThreads) fork_kernel(const __grid_constan
         if (blockIdx.y == 0 && threadIdx.x == 0) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
         return;
     }
-    const int vecs = (int)((size_t)tail * a.row_bytes / 16);
-    for (int p = blockIdx.y; p < a.n_pools; p += gridDim.y) {
-        char* pool = static_cast<char*>(pools.p[p]);
-        const uint4* from = reinterpret_cast<const uint4*>(pool + (size_t)src * a.page_bytes);
-        uint4* to = reinterpret_cast<uint4*>(pool + (size_t)base * a.page_bytes);
-        for (int i = threadIdx.x; i < vecs; i += kPageThreads) to[i] = from[i];
+    // this CTA's share of the pools as one long list of vectors, kCopies loads in
+    // flight per thread: a page's rows of one pool alone (2 to 30 KB) leave the
+    // memory waiting (72 pools, 45 slots: 17.3 us a pool per CTA, COPY_NEW us so)
+    const unsigned vecs = (unsigned)((size_t)tail * a.row_bytes / 16);
+    const int p0 = (int)((long long)a.n_pools * blockIdx.y / gridDim.y);
+    const int p1 = (int)((long long)a.n_pools * (blockIdx.y + 1) / gridDim.y);
+    const unsigned long long all = (unsigned long long)(p1 - p0) * vecs;
+    for (unsigned long long i0 = threadIdx.x; i0 < all; i0 += kCopies * kPageThreads) {
+        uint4 v[kCopies];
+        uint4* to[kCopies];
+#pragma unroll
+        for (int u = 0; u < kCopies; ++u) {
+            const unsigned long long i = i0 + u * kPageThreads;
+            if (i >= all) break;
+            const unsigned p = all >> 32 ? (unsigned)(i / vecs) : (unsigned)i / vecs, x = (unsigned)(i - (unsigned long long)p * vecs);
+            char* pool = static_cast<char*>(pools.p[p0 + p]);
+            v[u] = reinterpret_cast<const uint4*>(pool + (size_t)src * a.page_bytes)[x];
+            to[u] = reinterpret_cast<uint4*>(pool + (size_t)base * a.page_bytes) + x;
+        }
+#pragma unroll
+        for (int u = 0; u < kCopies; ++u)
+            if (i0 + u * kPageThreads < all) *to[u] = v[u];
     }
 }
 
@@ -176,6 +208,14 @@ struct CompactArgs {
     int32_t* moves;  // number of pages that move, then their old and new places
     int32_t* err_flag;
 };
+
+// Compaction, by the size of the bookkeeping: up to kSmallPages pages and
+// kSmallCells table cells one CTA does all of it with the bitmap in shared
+// memory (plan_small_kernel: 2 launches in all); beyond, mark, plan and place
+// are kernels of their own (5 with the bitmap's clearing).  The small way took
+// SMALL_A against SMALL_B us at 8 requests of 38 pages and SMALL_C against SMALL_D at
+// 64 of 4000 cells.
+constexpr int kSmallPages = 1 << 20, kSmallCells = 1 << 18, kSmallThreads = 1024;
 
 // One CTA per request: marks its pages.
 __global__ void __launch_bounds__(kPageThreads) mark_kernel(const __grid_constant__ CompactArgs a) {
@@ -193,6 +233,7 @@ __global__ void __launch_bounds__(kPageThreads) mark_kernel(const __grid_constan
 }
 
 // Exclusive scan over the CTA; returns the total.
+template <int THREADS>
 ISD_DEVINL int block_scan(int v, int& before, int* part) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int incl = v;
@@ -204,7 +245,7 @@ ISD_DEVINL int block_scan(int v, int& before, int* part) {
     if (lane == 31) part[warp] = incl;
     __syncthreads();
     int base = 0, total = 0;
-    for (int w = 0; w < kPageThreads / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) base += part[w];
         total += part[w];
     }
@@ -213,29 +254,29 @@ ISD_DEVINL int block_scan(int v, int& before, int* part) {
     return total;
 }
 
-// One CTA: L pages are in use; the k-th used page at or past L moves to the
-// k-th free place before L.
-__global__ void __launch_bounds__(kPageThreads) plan_kernel(const __grid_constant__ CompactArgs a) {
-    __shared__ int part[kPageThreads / 32];
+// L pages are in use; the k-th used page at or past L moves to the k-th free
+// place before L.  One CTA writes the list of moves.
+template <int THREADS>
+ISD_DEVINL int list_moves(const CompactArgs& a, const uint32_t* live, int* part) {
     const int words = (a.num_pages + 31) / 32;
     int count = 0;
-    for (int w0 = 0; w0 < words; w0 += kPageThreads) {
+    for (int w0 = 0; w0 < words; w0 += THREADS) {
         const int w = w0 + (int)threadIdx.x;
         int before;
-        count += block_scan(w < words ? __popc(a.live[w]) : 0, before, part);
+        count += block_scan<THREADS>(w < words ? __popc(live[w]) : 0, before, part);
     }
     int holes = 0, movers = 0;
     int32_t* src = a.moves + 1;
     int32_t* dst = src + a.num_pages;
-    for (int w0 = 0; w0 < words; w0 += kPageThreads) {
+    for (int w0 = 0; w0 < words; w0 += THREADS) {
         const int w = w0 + (int)threadIdx.x;
-        const uint32_t bits = w < words ? a.live[w] : 0;
+        const uint32_t bits = w < words ? live[w] : 0;
         // pages of this word that lie before / from L on
         const int below = min(max(count - 32 * w, 0), 32);
         const uint32_t low = below == 32 ? 0xffffffffu : ((1u << below) - 1);
         uint32_t h = w < words ? ~bits & low : 0, m = bits & ~low;
         int hb, mb;
-        const int ht = block_scan(__popc(h), hb, part), mt = block_scan(__popc(m), mb, part);
+        const int ht = block_scan<THREADS>(__popc(h), hb, part), mt = block_scan<THREADS>(__popc(m), mb, part);
         for (int k = holes + hb; h; h &= h - 1) dst[k++] = 32 * w + __ffs(h) - 1;
         for (int k = movers + mb; m; m &= m - 1) src[k++] = 32 * w + __ffs(m) - 1;
         holes += ht;
@@ -245,6 +286,41 @@ __global__ void __launch_bounds__(kPageThreads) plan_kernel(const __grid_constan
         a.moves[0] = movers;
         *a.next_free_out = count;
     }
+    return movers;
+}
+
+__global__ void __launch_bounds__(kPageThreads) plan_kernel(const __grid_constant__ CompactArgs a) {
+    __shared__ int part[kPageThreads / 32];
+    list_moves<kPageThreads>(a, a.live, part);
+}
+
+// Marking, listing and placing by one CTA.
+__global__ void __launch_bounds__(kSmallThreads) plan_small_kernel(const __grid_constant__ CompactArgs a) {
+    extern __shared__ uint32_t live[];
+    __shared__ int part[kSmallThreads / 32];
+    pdl_trigger();
+    const int words = (a.num_pages + 31) / 32, cells = a.B * a.max_pages;
+    for (int w = threadIdx.x; w < words; w += kSmallThreads) live[w] = 0;
+    for (int b = threadIdx.x; b < a.B; b += kSmallThreads) {
+        const int used = a.pages_used[b];
+        if (used < 0 || used > a.max_pages) raise_flag(a.err_flag, ISD_FLAG_CAPACITY);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int e = threadIdx.x; e < cells; e += kSmallThreads) {
+        const int b = e / a.max_pages, j = e - b * a.max_pages;
+        const int id = a.page_table[e];
+        if (j >= a.pages_used[b]) continue;
+        if (id < 0 || id >= a.num_pages) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
+        else atomicOr(&live[id >> 5], 1u << (id & 31));
+    }
+    __syncthreads();
+    const int n = list_moves<kSmallThreads>(a, live, part);
+    __syncthreads();
+    const int32_t* src = a.moves + 1;
+    const int32_t* dst = src + a.num_pages;
+    int32_t* to = a.moves + 1 + 2 * (size_t)a.num_pages;
+    for (int i = threadIdx.x; i < n; i += kSmallThreads) to[src[i]] = dst[i];
 }
 
 // New place of every page that moves, by its old one.
@@ -256,18 +332,19 @@ __global__ void __launch_bounds__(kPageThreads) place_kernel(const __grid_consta
     for (int i = blockIdx.x * kPageThreads + threadIdx.x; i < n; i += gridDim.x * kPageThreads) to[src[i]] = dst[i];
 }
 
-// The moves of all pools, one warp per piece of a page, and (with `tables`)
-// the page tables.
+// The moves of the pools (grid.y), one warp per piece of a page, and (with
+// `tables`) the page tables.
 constexpr int kMovePiece = 4096;
 __global__ void __launch_bounds__(kPageThreads) move_kernel(const __grid_constant__ CompactArgs a,
                                                             const __grid_constant__ PoolList pools, int tables) {
+    pdl_wait();
     const int n = a.moves[0];
     const int32_t* src = a.moves + 1;
     const int32_t* dst = src + a.num_pages;
     const int32_t* to = a.moves + 1 + 2 * (size_t)a.num_pages;
     const int live = *a.next_free_out;
     if (tables) {
-        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        for (int b = blockIdx.y * gridDim.x + blockIdx.x; b < a.B; b += gridDim.x * gridDim.y) {
             const int used = min(max(a.pages_used[b], 0), a.max_pages);
             for (int j = threadIdx.x; j < a.max_pages; j += kPageThreads) {
                 int id = -1;
@@ -279,21 +356,20 @@ __global__ void __launch_bounds__(kPageThreads) move_kernel(const __grid_constan
             }
         }
     }
+    if ((int)blockIdx.y >= a.n_pools) return;
     const int lane = threadIdx.x & 31;
-    const int pieces = (int)((a.page_bytes + kMovePiece - 1) / kMovePiece);
-    const long long items = (long long)n * pieces * a.n_pools;
-    const long long warps = (long long)gridDim.x * (kPageThreads / 32);
-    for (long long it = (long long)blockIdx.x * (kPageThreads / 32) + (threadIdx.x >> 5); it < items; it += warps) {
-        const int piece = (int)(it % pieces);
-        const long long q = it / pieces;
-        const int k = (int)(q % n), p = (int)(q / n);
-        char* pool = static_cast<char*>(pools.p[p]);
-        const size_t off = (size_t)piece * kMovePiece;
-        const uint4* from = reinterpret_cast<const uint4*>(pool + (size_t)src[k] * a.page_bytes + off);
-        uint4* dest = reinterpret_cast<uint4*>(pool + (size_t)dst[k] * a.page_bytes + off);
+    // a pool has fewer than 2^32 pieces: they hold 4 KB, or a page, of which there are fewer than 2^31
+    const uint32_t pieces = (uint32_t)((a.page_bytes + kMovePiece - 1) / kMovePiece);
+    const uint32_t items = n * pieces, warps = gridDim.x * (kPageThreads / 32);
+    char* pool = static_cast<char*>(pools.p[blockIdx.y]);
+    for (uint32_t it = blockIdx.x * (kPageThreads / 32) + (threadIdx.x >> 5); it < items; it += warps) {
+        const uint32_t k = it / pieces;
+        const size_t off = (size_t)(it - k * pieces) * kMovePiece;
         const size_t left = a.page_bytes - off;
-        const int vecs = (int)((left < kMovePiece ? left : kMovePiece) / 16);
-        for (int i = lane; i < vecs; i += 32) dest[i] = from[i];
+        copy_vecs(reinterpret_cast<const uint4*>(pool + (size_t)src[k] * a.page_bytes + off),
+                  reinterpret_cast<uint4*>(pool + (size_t)dst[k] * a.page_bytes + off),
+                  (int)((left < kMovePiece ? left : kMovePiece) / 16), lane, 32);
+        if (it + warps < it) break;  // past 2^32
     }
 }
 
@@ -328,7 +404,9 @@ cudaError_t launch_fork(const isd_dims* d, int R, const int32_t* parent, const i
         PoolList list;
         a.n_pools = n_pools - p0 < kPoolsPerLaunch ? n_pools - p0 : kPoolsPerLaunch;
         for (int i = 0; i < a.n_pools; ++i) list.p[i] = pools[p0 + i];
-        const cudaError_t e = launch_kernel(false, fork_kernel, dim3(R, a.n_pools > 0 ? a.n_pools : 1),
+        // as many CTAs as run at once (3 an SM): each first works out the slots before its own
+        const int shares = std::max(1, std::min(a.n_pools, 3 * persistent_grid() / R));
+        const cudaError_t e = launch_kernel(false, fork_kernel, dim3(R, shares),
                                             dim3(kPageThreads), (size_t)d->B * 4, st, a, list);
         if (e != cudaSuccess) return e;
     }
@@ -350,19 +428,39 @@ cudaError_t launch_compact(const isd_dims* d, const int32_t* pages_used, const i
     a.live = static_cast<uint32_t*>(ws);
     a.moves = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + align_up((size_t)(d->num_pages + 31) / 32 * 4, 256));
     a.err_flag = err_flag;
-    cudaError_t e = cudaMemsetAsync(a.live, 0, (size_t)(d->num_pages + 31) / 32 * 4, st);
-    if (e != cudaSuccess) return e;
-    e = launch_kernel(false, mark_kernel, dim3(d->B), dim3(kPageThreads), 0, st, a);
-    if (e != cudaSuccess) return e;
-    e = launch_kernel(false, plan_kernel, dim3(1), dim3(kPageThreads), 0, st, a);
-    if (e != cudaSuccess) return e;
-    e = launch_kernel(false, place_kernel, dim3(persistent_grid()), dim3(kPageThreads), 0, st, a);
-    if (e != cudaSuccess) return e;
+    const size_t bitmap = (size_t)(d->num_pages + 31) / 32 * 4;
+    const bool small = d->num_pages <= kSmallPages && (long long)d->B * d->max_pages_per_req <= kSmallCells;
+    cudaError_t e;
+    if (small) {
+        static unsigned long long configured = 0;  // bit per device
+        int dev = 0;
+        e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        if (!(configured >> dev & 1ull)) {
+            e = cudaFuncSetAttribute(plan_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallPages / 8);
+            if (e != cudaSuccess) return e;
+            configured |= 1ull << dev;
+        }
+        e = launch_kernel(false, plan_small_kernel, dim3(1), dim3(kSmallThreads), bitmap, st, a);
+        if (e != cudaSuccess) return e;
+    } else {
+        e = cudaMemsetAsync(a.live, 0, bitmap, st);
+        if (e != cudaSuccess) return e;
+        e = launch_kernel(false, mark_kernel, dim3(d->B), dim3(kPageThreads), 0, st, a);
+        if (e != cudaSuccess) return e;
+        e = launch_kernel(false, plan_kernel, dim3(1), dim3(kPageThreads), 0, st, a);
+        if (e != cudaSuccess) return e;
+        e = launch_kernel(false, place_kernel, dim3(persistent_grid()), dim3(kPageThreads), 0, st, a);
+        if (e != cudaSuccess) return e;
+    }
     for (int p0 = 0; p0 == 0 || p0 < n_pools; p0 += kPoolsPerLaunch) {
         PoolList list;
         a.n_pools = n_pools - p0 < kPoolsPerLaunch ? n_pools - p0 : kPoolsPerLaunch;
         for (int i = 0; i < a.n_pools; ++i) list.p[i] = pools[p0 + i];
-        e = launch_kernel(false, move_kernel, dim3(8 * persistent_grid()), dim3(kPageThreads), 0, st, a, list, p0 == 0 ? 1 : 0);
+        const int rows = a.n_pools > 0 ? a.n_pools : 1;
+        e = launch_kernel(small && p0 == 0, move_kernel, dim3((8 * persistent_grid() + rows - 1) / rows, rows),
+                          dim3(kPageThreads), 0, st, a, list, p0 == 0 ? 1 : 0);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

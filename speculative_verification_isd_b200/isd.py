@@ -547,19 +547,42 @@ def embed_block(d: Dims, E, n_clean, clean_tok, x, err_flag=None, stream=None):
 # ---------------------------------------------------------------------------
 # Prompts and pages
 # ---------------------------------------------------------------------------
-def _on_device(tensors, stream):
-    """The tensors' one device, made current for the call, and the stream to
-    use there: a CUDA launch takes both from the calling thread."""
-    dev = None
-    for name, t in tensors:
+_I32 = torch.int32
+# the current stream's handle, without a Stream object around it where torch offers that
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _pointers(named):
+    """Pointers of (name, tensor, dtype, numel) on one device, checked like
+    _ptr does, and that device's index."""
+    dev, ptrs = None, []
+    for name, t, dtype, n in named:
         if t is None:
+            ptrs.append(None)
             continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-    return torch.cuda.device(dev), \
-        torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+        i = t.get_device()
+        if i < 0 or t.dtype != dtype or (n is not None and t.numel() != n) or not t.is_contiguous():
+            _ptr(t, _BF16 if dtype == torch.bfloat16 else dtype, n, name)
+        if i != dev:
+            if dev is not None:
+                raise ValueError(f"{name} is on cuda:{i}, the other tensors on cuda:{dev}")
+            dev = i
+        ptrs.append(t.data_ptr())
+    return ptrs, dev
+
+
+def _call_on(dev, stream, fn, *args):
+    """fn(*args, stream) with the tensors' device current: a CUDA launch takes
+    device and stream from the calling thread."""
+    st = _current_stream(dev) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, st)
+    if status != ISD_OK:
+        raise IsdError(status)
 
 
 def chunk_workspace_bytes(d: Dims, T: int) -> int:
@@ -588,32 +611,21 @@ class ChunkCall:
         if d.Hq < 1 or d.Hkv < 1 or d.D < 1:
             raise IsdError(ISD_ERR_INVALID_ARG)
         T = q.numel() // (d.Hq * d.D)
-        kvrow = d.page_size * d.Hkv * d.D
+        kvrow, bf16 = d.page_size * d.Hkv * d.D, torch.bfloat16
         named = [
-            ("q", q, _BF16, T * d.Hq * d.D), ("k_new", k_new, _BF16, T * d.Hkv * d.D),
-            ("v_new", v_new, _BF16, T * d.Hkv * d.D), ("k_pool", k_pool, _BF16, d.num_pages * kvrow),
-            ("v_pool", v_pool, _BF16, d.num_pages * kvrow),
-            ("page_table", page_table, torch.int32, d.B * d.max_pages_per_req),
-            ("kv_len", kv_len, torch.int32, d.B), ("q_start", q_start, torch.int32, d.B + 1),
-            ("out", out, _BF16, T * d.Hq * d.D), ("ws", ws, torch.uint8, None)]
-        ptrs = [_ptr(t, dt, n, name) for name, t, dt, n in named]
-        flag = _ptr(err_flag, torch.int32, 1, "err_flag")
-        tensors = [(name, t) for name, t, _, _ in named] + [("err_flag", err_flag)]
-        _on_device(tensors, stream)
-        self._keep = (d, tensors)  # the cached arguments point at them
-        self._device = q.device
-        self._stream = None if stream is None else _stream(stream)
-        self._args = (ctypes.byref(d), T, *ptrs, ws.numel(), flag)
+            ("q", q, bf16, T * d.Hq * d.D), ("k_new", k_new, bf16, T * d.Hkv * d.D),
+            ("v_new", v_new, bf16, T * d.Hkv * d.D), ("k_pool", k_pool, bf16, d.num_pages * kvrow),
+            ("v_pool", v_pool, bf16, d.num_pages * kvrow),
+            ("page_table", page_table, _I32, d.B * d.max_pages_per_req),
+            ("kv_len", kv_len, _I32, d.B), ("q_start", q_start, _I32, d.B + 1),
+            ("out", out, bf16, T * d.Hq * d.D), ("ws", ws, torch.uint8, None)]
+        ptrs, self._dev = _pointers(named + [("err_flag", err_flag, _I32, 1)])
+        self._keep = (d, named, err_flag)  # the cached arguments point at them
+        self._stream = stream
+        self._args = (ctypes.byref(d), T, *ptrs[:-1], ws.numel(), ptrs[-1])
 
     def __call__(self):
-        st = self._stream
-        if st is None:
-            st = torch.cuda.current_stream(self._device).cuda_stream
-        if torch.cuda.current_device() == self._device.index:
-            _check(_lib.isd_chunk_attention(*self._args, st))
-        else:
-            with torch.cuda.device(self._device):
-                _check(_lib.isd_chunk_attention(*self._args, st))
+        _call_on(self._dev, self._stream, _lib.isd_chunk_attention, *self._args)
 
 
 def chunk_attention(d: Dims, q, k_new, v_new, k_pool, v_pool, page_table, kv_len, q_start, out, ws,
@@ -631,13 +643,10 @@ class PoolArray:
     def __init__(self, d: Dims, pools):
         pools = list(pools)
         kvrow = d.page_size * d.Hkv * d.D
-        self.ptrs = (_vp * max(len(pools), 1))()
         self.count = len(pools)
         self.numel = d.num_pages * kvrow
-        for i, t in enumerate(pools):
-            self.ptrs[i] = _ptr(t, _BF16, self.numel, f"pool {i}")
-            if t.device != pools[0].device:
-                raise ValueError(f"pool {i} is on {t.device}, pool 0 on {pools[0].device}")
+        ptrs, self.dev = _pointers([(f"pool {i}", t, torch.bfloat16, self.numel) for i, t in enumerate(pools)])
+        self.ptrs = (_vp * max(len(pools), 1))(*ptrs)
         self.tensors = pools  # keeps them alive
 
 
@@ -655,6 +664,11 @@ def _pools(d: Dims, pools) -> PoolArray:
     return pools
 
 
+def _same_device(pa: PoolArray, dev):
+    if pa.count and pa.dev != dev:
+        raise ValueError(f"the pools are on cuda:{pa.dev}, the other tensors on cuda:{dev}")
+
+
 def fork_requests(d: Dims, parent, kv_len, pages_used, page_table, next_free_page, pools,
                   next_kv_len, next_pages_used, next_page_table, next_free_out, reserve=None,
                   err_flag=None, stream=None):
@@ -662,21 +676,15 @@ def fork_requests(d: Dims, parent, kv_len, pages_used, page_table, next_free_pag
     (-1: empty), with room for reserve[r] more tokens.  pools: every layer's
     k_pool and v_pool (an iterable of tensors, or a pool_array)."""
     R, cols = parent.numel(), d.max_pages_per_req
-    pa = _pools(d, pools)
-    i32 = torch.int32
-    named = [("parent", parent, R), ("reserve", reserve, R), ("kv_len", kv_len, d.B),
-             ("pages_used", pages_used, d.B), ("page_table", page_table, d.B * cols),
-             ("next_free_page", next_free_page, 1)]
-    outs = [("next_kv_len", next_kv_len, R), ("next_pages_used", next_pages_used, R),
-            ("next_page_table", next_page_table, R * cols), ("next_free_out", next_free_out, 1)]
-    p_in = [_ptr(t, i32, n, name) for name, t, n in named]
-    p_out = [_ptr(t, i32, n, name) for name, t, n in outs]
-    flag = _ptr(err_flag, i32, 1, "err_flag")
-    guard, st = _on_device([(name, t) for name, t, _ in named + outs] + [("err_flag", err_flag)] +
-                           [("pools", t) for t in pa.tensors[:1]], stream)
-    with guard:
-        _check(_lib.isd_fork_requests(ctypes.byref(d), R, *p_in, pa.count, pa.ptrs, *p_out, flag,
-                                      st))
+    pa, i32 = _pools(d, pools), _I32
+    p, dev = _pointers([
+        ("parent", parent, i32, R), ("reserve", reserve, i32, R), ("kv_len", kv_len, i32, d.B),
+        ("pages_used", pages_used, i32, d.B), ("page_table", page_table, i32, d.B * cols),
+        ("next_free_page", next_free_page, i32, 1), ("next_kv_len", next_kv_len, i32, R),
+        ("next_pages_used", next_pages_used, i32, R), ("next_page_table", next_page_table, i32, R * cols),
+        ("next_free_out", next_free_out, i32, 1), ("err_flag", err_flag, i32, 1)])
+    _same_device(pa, dev)
+    _call_on(dev, stream, _lib.isd_fork_requests, ctypes.byref(d), R, *p[:6], pa.count, pa.ptrs, *p[6:])
 
 
 def pages_workspace_bytes(d: Dims) -> int:
@@ -695,16 +703,11 @@ def compact_pages(d: Dims, page_table, pages_used, pools, next_page_table, next_
                   err_flag=None, stream=None):
     """isd_compact_pages: the pages in use become pages 0 .. L-1 of every pool
     (next_free_out = L); next_page_table is the table after the move."""
-    pa = _pools(d, pools)
-    i32, n = torch.int32, d.B * d.max_pages_per_req
-    named = [("pages_used", pages_used, i32, d.B), ("page_table", page_table, i32, n)]
-    outs = [("next_page_table", next_page_table, i32, n), ("next_free_out", next_free_out, i32, 1),
-            ("ws", ws, torch.uint8, None)]
-    p_in = [_ptr(t, dt, k, name) for name, t, dt, k in named]
-    p_out = [_ptr(t, dt, k, name) for name, t, dt, k in outs]
-    flag = _ptr(err_flag, i32, 1, "err_flag")
-    guard, st = _on_device([(name, t) for name, t, _, _ in named + outs] +
-                           [("err_flag", err_flag)] + [("pools", t) for t in pa.tensors[:1]], stream)
-    with guard:
-        _check(_lib.isd_compact_pages(ctypes.byref(d), *p_in, pa.count, pa.ptrs, *p_out,
-                                      ws.numel(), flag, st))
+    pa, i32, n = _pools(d, pools), _I32, d.B * d.max_pages_per_req
+    p, dev = _pointers([
+        ("pages_used", pages_used, i32, d.B), ("page_table", page_table, i32, n),
+        ("next_page_table", next_page_table, i32, n), ("next_free_out", next_free_out, i32, 1),
+        ("ws", ws, torch.uint8, None), ("err_flag", err_flag, i32, 1)])
+    _same_device(pa, dev)
+    _call_on(dev, stream, _lib.isd_compact_pages, ctypes.byref(d), *p[:2], pa.count, pa.ptrs, *p[2:5],
+             ws.numel(), p[5])
