@@ -529,16 +529,20 @@ isd_status isd_layers(const isd_dims* d, int32_t n_layers, int32_t inter, float 
  *          written.
  * What a cache row at or past a request's last position holds is not read
  * into any result (it may be NaN); nor is a key or value that a row's causal
- * mask hides.
+ * mask hides.  A row that sees a NaN or an infinity comes out non-finite where
+ * it counts (an infinite value of V as that infinity or as NaN).
+ * The rows that the call writes must not be among the cached ones (positions
+ * below kv_len) of another of its requests: the two are not ordered.
  * Supported: D in {64, 128}, Hq/Hkv <= 128.  N and V of the dims are not used
  * (any positive values).  Workspace: isd_chunk_workspace_bytes(d, T) bytes,
  * 256-aligned (0 for invalid dims or T < 0); one made for a larger T serves.
- * Errors: a null pointer, invalid dims, T < 0 or an sm_scale that is not
- * positive and finite -> ISD_ERR_INVALID_ARG (a tensor not 16-byte aligned too); a shape not supported ->
+ * Errors: a null pointer, invalid dims, T < 0, an sm_scale that is not
+ * positive and finite, a tensor that is not 16-byte aligned, or an out that
+ * overlaps an input -> ISD_ERR_INVALID_ARG; a shape not supported ->
  * ISD_ERR_UNSUPPORTED_SHAPE; a workspace too small or misaligned ->
  * ISD_ERR_WORKSPACE.  On the device: ISD_FLAG_CHUNK_RANGE (no request is
  * served); ISD_FLAG_CAPACITY (a request with a negative kv_len or tokens past
- * its pages: its rows of out are zero, its cache is left alone);
+ * its pages or 2^30: its rows of out are zero, its cache is left alone);
  * ISD_FLAG_PAGE_OOB (keys and values on a page id outside the pool read as
  * zeros, and are not written).  Two calls may overlap on the GPU if their
  * workspaces and the cache rows they write differ.
@@ -598,6 +602,7 @@ isd_status isd_fork_requests(const isd_dims* d, int32_t R, const int32_t* parent
  *   (every pool moves the same pages)
  *   next_page_table [B, max_pages_per_req] int32 (may be page_table itself):
  *          the table after the move, -1 past pages_used; next_free_out [1] = L
+ * (Otherwise the outputs overlap no input and not each other.)
  * A page that several requests share moves once.  Pages from L on keep their
  * bytes, so the call can be repeated on the same inputs.
  * Workspace: isd_pages_workspace_bytes(d) bytes, 256-aligned.  Supported as

@@ -54,6 +54,7 @@ constexpr int kHalfBytes = kKeys * 128; // 64 dimensions of a K, V or Q tile
 // (a TMA copy takes the producer about 70 cycles to issue).
 constexpr int kGroupRows = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr long long kMaxKeys = 1ll << 30;  // of a request: positions and tiles fit in 32 bits
 // New tokens that are put into the free rows of the last cached tile instead
 // of a tile of their own.
 constexpr int kMergeTokens = 16;
@@ -93,12 +94,12 @@ struct ChunkArgs {
     int32_t* err_flag;
 };
 
-// New tokens of request b if its page list can hold them, else 0 (negative
+// New tokens of a request if its page list can hold them, else 0 (negative
 // or over-capacity length).  q_start is known to ascend within [0, T].
 ISD_DEVINL int chunk_tokens(const ChunkArgs& a, int kv, int n) {
     if (kv < 0) return 0;
     const long long t = (long long)kv + n;
-    return t > (long long)a.max_pages * a.P ? 0 : n;
+    return t > (long long)a.max_pages * a.P || t > kMaxKeys ? 0 : n;
 }
 
 // A request as the partition sees it.
@@ -1001,11 +1002,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const bool live = rr < (quad ? a.tps : a.tpq) * a.grp && i < p.i1;
             const int step = p.mode == kTwo ? 1 : 2, t_first = p.t0 + (p.mode == kTwo ? 0 : wg);
             float m_ref = -INFINITY, l = 0.f;
-            // the row's maximum is top: the reference (a whole number, so that what
-            // is scaled to another one stays as it is), l, and O if it holds
-            // products, follow
+            // the row's maximum is top: the reference, l, and O if it holds products,
+            // follow (the maximum's own weight is then 1, which bf16 holds exactly)
             auto move_ref = [&](float top, bool has_o) {
-                const float m_new = fmaxf(m_ref, ceilf(top));
+                const float m_new = fmaxf(m_ref, top);
                 const float f = m_new > m_ref ? ex2(m_ref - m_new) : 1.f;
                 if (has_o) {
 #pragma unroll 1

@@ -756,6 +756,11 @@ isd_status isd_chunk_attention(const isd_dims* d, int32_t T, const uint16_t* q,
     if (d->D != 64 && d->D != 128) return unsupported("head dim must be 64 or 128");
     if (d->Hq / d->Hkv > 128) return unsupported("Hq/Hkv must be <= 128");
     if (T == 0) return ISD_OK;
+    const size_t out_n = (size_t)T * d->Hq * d->D * 2, new_n = (size_t)T * d->Hkv * d->D * 2;
+    const size_t pool_n = (size_t)d->num_pages * d->page_size * d->Hkv * d->D * 2;
+    if (overlaps(out, out_n, q, out_n) || overlaps(out, out_n, k_new, new_n) || overlaps(out, out_n, v_new, new_n) ||
+        overlaps(out, out_n, k_pool, pool_n) || overlaps(out, out_n, v_pool, pool_n))
+        return invalid("out overlaps an input");
     ISD_CUDA(isd::launch_chunk_attention(d, T, q, k_new, v_new, k_pool, v_pool, page_table, kv_len,
                                          q_start, out, ws, err_flag, static_cast<cudaStream_t>(stream)));
     return ISD_OK;
@@ -802,6 +807,11 @@ isd_status isd_compact_pages(const isd_dims* d, const int32_t* pages_used,
     ISD_TRY(check_ws_bytes(isd::pages_ws_bytes(d), ws, ws_bytes));
     if (!pages_used || !page_table || !next_page_table || !next_free_out)
         return invalid("null compact pointer");
+    const size_t table_n = (size_t)d->B * d->max_pages_per_req * 4, used_n = (size_t)d->B * 4;
+    if ((next_page_table != page_table && overlaps(next_page_table, table_n, page_table, table_n)) ||
+        overlaps(next_page_table, table_n, pages_used, used_n) || overlaps(next_free_out, 4, pages_used, used_n) ||
+        overlaps(next_free_out, 4, page_table, table_n) || overlaps(next_free_out, 4, next_page_table, table_n))
+        return invalid("a compact output overlaps an input or the other one");
     ISD_TRY(check_pools(d, n_pools, pools));
     ISD_CUDA(isd::launch_compact(d, pages_used, page_table, n_pools, pools, next_page_table,
                                  next_free_out, ws, err_flag, static_cast<cudaStream_t>(stream)));

@@ -108,6 +108,15 @@ def test_chunk_refusals(isd):
     for scale in (0.0, -1.0, math.inf, math.nan):
         assert call(dd=_dims(isd, sm_scale=scale)) == isd.ISD_ERR_INVALID_ARG, scale
     assert lib.isd_chunk_attention(None, 1, *[fake] * 9, fake, need, None, None) == isd.ISD_ERR_INVALID_ARG
+    # an output on top of an input (q, k_new, v_new, a pool's last row)
+    at = lambda k: ctypes.c_void_p((1 + k) << 24)  # noqa: E731
+    for i in (0, 1, 2, 3, 4):
+        p = [at(k) for k in range(9)]
+        p[8] = ctypes.c_void_p(p[i].value + 16)
+        assert call(p=p) == isd.ISD_ERR_INVALID_ARG, i
+    p = [at(k) for k in range(9)]
+    p[8] = ctypes.c_void_p(p[4].value + d.num_pages * d.page_size * 2 * 128 * 2 - 16)
+    assert call(p=p) == isd.ISD_ERR_INVALID_ARG
     # no rows: nothing to do, and nothing is launched
     assert call(T=0) == isd.ISD_OK
 
@@ -153,7 +162,9 @@ def test_compact_refusals(isd):
     assert need > 0 and need % 256 == 0
     pools = (ctypes.c_void_p * 1)(1 << 30)
 
-    def call(dd=d, p=(fake, fake), n=1, pools=pools, o=(fake, fake), ws=fake, k=need):
+    other, free = ctypes.c_void_p(2 << 20), ctypes.c_void_p(3 << 20)
+
+    def call(dd=d, p=(other, fake), n=1, pools=pools, o=(fake, free), ws=fake, k=need):
         return lib.isd_compact_pages(ctypes.byref(dd), *p, n, pools, *o, ws, k, None, None)
 
     assert call(p=(None, fake)) == isd.ISD_ERR_INVALID_ARG
@@ -162,6 +173,11 @@ def test_compact_refusals(isd):
     assert call(o=(fake, None)) == isd.ISD_ERR_INVALID_ARG
     assert call(n=-1) == isd.ISD_ERR_INVALID_ARG
     assert call(pools=(ctypes.c_void_p * 1)(None)) == isd.ISD_ERR_INVALID_ARG
+    # the new table may be the old one, but not lie across it; nothing else overlaps
+    assert call(o=(ctypes.c_void_p((1 << 20) + 4), free)) == isd.ISD_ERR_INVALID_ARG
+    assert call(o=(other, free)) == isd.ISD_ERR_INVALID_ARG
+    for p in (other, fake, ctypes.c_void_p((1 << 20) + 8)):
+        assert call(o=(fake, p)) == isd.ISD_ERR_INVALID_ARG
     assert call(ws=None) == isd.ISD_ERR_WORKSPACE
     assert call(k=need - 1) == isd.ISD_ERR_WORKSPACE
     assert call(ws=ctypes.c_void_p((1 << 20) + 4)) == isd.ISD_ERR_WORKSPACE

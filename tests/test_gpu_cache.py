@@ -156,6 +156,29 @@ LONG = {
 }
 
 
+def test_chunk_one_key_is_its_value(isd):
+    """A row with one key is that key's value to the last bit."""
+    c = Chunk(isd, 8, 2, 128, 16, [0] * 5, [1, 1, 3, 1, 20], seed=2, gain=7.0).upload().call().check()
+    first = [c.start[b] for b in range(5)]
+    got = c.out.view(-1, 8, 128)[first]
+    assert torch.equal(got, c.d_in[2][first].repeat_interleave(4, 1))
+
+
+def test_chunk_more_requests_than_threads(isd):
+    """The cut of the work goes over the requests in several rounds, twice."""
+    B = 900
+    ctx = [(7 * b) % 90 for b in range(B)]
+    n = [0 if b % 3 else 1 + b % 2 for b in range(B)]
+    n[-1], ctx[-1] = 40, 300
+    Chunk(isd, 4, 2, 64, 16, ctx, n, seed=5, after=3).upload().call().check()
+
+
+def test_chunk_one_long_request_many_parts(isd):
+    """One KV head over a long context: the item is cut between all CTAs."""
+    Chunk(isd, 8, 1, 128, 64, [30011], [2], seed=6).upload().call().check()
+    Chunk(isd, 4, 1, 64, 16, [18000], [20], seed=7).upload().call().check()
+
+
 @pytest.mark.parametrize("gain", [1.0, 20.0])
 @pytest.mark.parametrize("name", LONG)
 def test_chunk_long_pieces(isd, name, gain):
@@ -471,6 +494,27 @@ def test_compact_many_shared_pages(isd):
         c.table[b + 1, :n] = c.table[b, :n]
     c.used = [u if rng.random() < 0.6 else 0 for u in c.used]
     check_compact(isd, c)
+
+
+@pytest.mark.parametrize("B,cols,pages", [(300, 900, 3000), (4, 20, (1 << 20) + 77)])
+def test_compact_large_bookkeeping(isd, B, cols, pages):
+    """More table cells, or more pages, than one CTA takes on."""
+    rng = np.random.default_rng(9)
+    c = Cache(isd, B, 1, rng.integers(0, 9, B), layers=1, Hkv=1, D=8, spare=0, cols=cols, seed=9)
+    c.pages = pages
+    ids = rng.permutation(pages)[:sum(c.used)]
+    at = 0
+    for b, u in enumerate(c.used):
+        c.table[b, :u] = ids[at:at + u]
+        at += u
+    c.dims = isd.make_dims(B, 1, 1, 1, 8, 1, 1, pages, cols)
+    c.pools = [bf16(rng, pages, 1, 1, 8).cuda() for _ in range(2)]
+    c.used = [u if b % 3 else 0 for b, u in enumerate(c.used)]
+    check_compact(isd, c)
+    c.err.zero_()
+    c.table[1, 0] = -7
+    c.used[1] = max(c.used[1], 1)
+    check_compact(isd, c, flags=isd.FLAG_PAGE_OOB, in_place=True)
 
 
 def test_compact_faults(isd):
