@@ -575,7 +575,7 @@ isd_status isd_chunk_attention(const isd_dims* d, int32_t T, const uint16_t* q,
  *  - Of the pools, only pages from *next_free_page on are written.  Nothing of
  *    the old batch's state changes: the call can be repeated, or the new state
  *    be thrown away.
- * Supported: page bytes (Hkv * D * 2 per token) a multiple of 16; B <= 12000.
+ * Supported: Hkv * D * 2 bytes (a token) a multiple of 16; B + R <= 12000.
  * N, V, Hq and sm_scale are not used.
  * Errors: invalid dims, R < 1, n_pools < 0, a null or misaligned pointer, an
  * output that is also an input -> ISD_ERR_INVALID_ARG; else

@@ -779,7 +779,7 @@ isd_status isd_fork_requests(const isd_dims* d, int32_t R, const int32_t* parent
         !next_pages_used || !next_page_table || !next_free_out)
         return invalid("null fork pointer");
     ISD_TRY(check_pools(d, n_pools, pools));
-    if (d->B > 12000) return unsupported("B must be <= 12000");
+    if ((int64_t)d->B + R > 12000) return unsupported("B + R must be <= 12000");
     const size_t cols = (size_t)d->max_pages_per_req * 4, b4 = (size_t)d->B * 4, r4 = (size_t)R * 4;
     const void* in[6] = {parent, reserve, kv_len, pages_used, page_table, next_free_page};
     const size_t in_n[6] = {r4, reserve ? r4 : 0, b4, b4, d->B * cols, 4};

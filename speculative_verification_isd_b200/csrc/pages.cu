@@ -14,7 +14,8 @@ namespace isd {
 namespace {
 
 constexpr int kPageThreads = 256;
-constexpr int kCopies = 8;  // 16-byte loads in flight per thread of a fork's copy
+constexpr int kCopies = 8;     // 16-byte loads in flight per thread of a fork's copy
+constexpr int kForkPools = 4;  // pools of one copy
 
 struct ForkArgs {
     int B, R, P, num_pages, max_pages, n_pools;
@@ -78,46 +79,74 @@ ISD_DEVINL void copy_vecs(const uint4* __restrict__ from, uint4* __restrict__ to
     for (; i < vecs; i += step) to[i] = from[i];
 }
 
-template <typename T>
-ISD_DEVINL T block_sum(T v, T* part) {
+// Exclusive scan over the CTA; returns the total.
+template <int THREADS, typename T>
+ISD_DEVINL T block_scan(T v, T& before, T* part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T incl = v;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    for (int off = 1; off < 32; off <<= 1) {
+        const T u = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += u;
+    }
+    if (lane == 31) part[warp] = incl;
     __syncthreads();
-    T t = 0;
-    for (int i = 0; i < kPageThreads / 32; ++i) t += part[i];
+    T base = 0, total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) base += part[w];
+        total += part[w];
+    }
     __syncthreads();
-    return t;
+    before = base + incl - v;
+    return total;
 }
 
-// grid (R, shares of the pools): every CTA works out its child's new pages
-// (the counts of the children before it, in slot order), the first piece
-// writes the child's state, and all copy the part-filled last page.
+// Every CTA works out all children's new pages (a scan in slot order), then
+// takes its share: the state and table row of some children, and of the
+// part-filled pages' copies some (child, group of pools) pairs.
+//
+// A copy is latency: a child's rows of one pool are 2 to 30 KB.  So the pairs,
+// whose bytes go from none to a page's, are dealt out in turn (a grid of (child,
+// share of the pools) left the CTAs of the longest tail running alone: 18.6
+// against FORK_NEW us for 45 slots and 72 pools), and a thread has kCopies loads in flight
+// over the pools of a pair.
 __global__ void __launch_bounds__(kPageThreads, 3) fork_kernel(const __grid_constant__ ForkArgs a,
-                                                            const __grid_constant__ PoolList pools) {
+                                                               const __grid_constant__ PoolList pools) {
     extern __shared__ int first_of[];  // [B]: the first child of each request
+    int* page_of = first_of + a.B;     // [R]: each child's first new page, or -1 where it cannot be made
     __shared__ long long part[kPageThreads / 32];
-    const int r = blockIdx.x;
+    __shared__ int s_end;
     for (int b = threadIdx.x; b < a.B; b += kPageThreads) first_of[b] = a.R;
+    if (threadIdx.x == 0) s_end = max(*a.next_free, 0);
     __syncthreads();
     for (int i = threadIdx.x; i < a.R; i += kPageThreads) {
         const int p = a.parent[i];
         if (p >= 0 && p < a.B) atomicMin(&first_of[p], i);
     }
     __syncthreads();
-    long long before = 0;
-    for (int i = threadIdx.x; i < r; i += kPageThreads) {
-        const Child c = child_of(a, first_of, i);
-        before += c.need - c.have;
+    long long run = max(*a.next_free, 0);
+    for (int i0 = 0; i0 < a.R; i0 += kPageThreads) {
+        const int i = i0 + (int)threadIdx.x;
+        const Child c = i < a.R ? child_of(a, first_of, i) : Child{-1, 0, 0, 0, false, 0};
+        const long long add = c.need - c.have;
+        long long before;
+        const long long sum = block_scan<kPageThreads>(add, before, part);
+        const long long base = run + before;
+        // a child past the pool's end gets no pages, nor does any after it that needs some
+        const bool fits = add == 0 || base + add <= a.num_pages;
+        if (i < a.R) page_of[i] = fits ? (int)min(base, (long long)a.num_pages) : -1;
+        if (add > 0 && fits) atomicMax(&s_end, (int)(base + add));
+        run += sum;
     }
-    before = block_sum(before, part);
-    Child c = child_of(a, first_of, r);
-    const long long free0 = max(*a.next_free, 0);
-    const long long base = free0 + before;
-    if (c.need > c.have && base + (c.need - c.have) > a.num_pages) {
-        c = Child{-1, 0, 0, 0, false, ISD_FLAG_CAPACITY};
-    }
-    if (blockIdx.y == 0) {
+    __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.next_free_out = s_end;
+    auto child = [&](int r) {
+        const Child c = child_of(a, first_of, r);
+        return page_of[r] < 0 ? Child{-1, 0, 0, 0, false, ISD_FLAG_CAPACITY} : c;
+    };
+    for (int r = blockIdx.x; r < a.R; r += gridDim.x) {
+        const Child c = child(r);
+        const int base = page_of[r];
         if (threadIdx.x == 0) {
             if (c.fault) raise_flag(a.err_flag, c.fault);
             a.next_kv_len[r] = c.kv;
@@ -129,71 +158,43 @@ __global__ void __launch_bounds__(kPageThreads, 3) fork_kernel(const __grid_cons
                 id = a.page_table[(size_t)c.par * a.max_pages + j];
                 if (id < 0 || id >= a.num_pages) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
             } else if (j < c.need) {
-                id = (int)(base + (j - c.have));
+                id = base + (j - c.have);
             }
             a.next_table[(size_t)r * a.max_pages + j] = id;
         }
-        if (r == a.R - 1) {
-            // pages handed out: the end of the last child that fits (the
-            // children after one that does not fit get none either)
-            __shared__ long long s_end;
-            if (threadIdx.x == 0) s_end = free0;
-            __syncthreads();
-            long long run = free0;
-            for (int i0 = 0; i0 < a.R; i0 += kPageThreads) {
-                const int i = i0 + (int)threadIdx.x;
-                int add = 0;
-                if (i < a.R) {
-                    const Child k = child_of(a, first_of, i);
-                    add = k.need - k.have;
-                }
-                long long incl = add;
+    }
+    // the part-filled pages: the rows before kv_len go to the child's own page
+    const int groups = (a.n_pools + kForkPools - 1) / kForkPools;
+    for (long long w = blockIdx.x; w < (long long)a.R * groups; w += gridDim.x) {
+        const int r = (int)(w / groups), p0 = (int)(w - (long long)r * groups) * kForkPools;
+        const Child c = child(r);
+        const int tail = c.par >= 0 && !c.first ? c.kv % a.P : 0;
+        if (tail == 0) continue;
+        const int src = a.page_table[(size_t)c.par * a.max_pages + c.have];
+        if (src < 0 || src >= a.num_pages) {
+            if (p0 == 0 && threadIdx.x == 0) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
+            continue;
+        }
+        const size_t from = (size_t)src * a.page_bytes, to = (size_t)page_of[r] * a.page_bytes;
+        const size_t vecs = (size_t)tail * a.row_bytes / 16, all = min(kForkPools, a.n_pools - p0) * vecs;
+        for (size_t i0 = threadIdx.x; i0 < all; i0 += kCopies * kPageThreads) {
+            uint4 v[kCopies];
+            uint4* dst[kCopies];
 #pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const long long v = __shfl_up_sync(0xffffffffu, incl, off);
-                    if ((int)(threadIdx.x & 31) >= off) incl += v;
-                }
-                if ((threadIdx.x & 31) == 31) part[threadIdx.x >> 5] = incl;
-                __syncthreads();
-                for (int w = 0; w < (int)(threadIdx.x >> 5); ++w) incl += part[w];
-                const long long end = run + incl;
-                if (add > 0 && end <= a.num_pages) atomicMax(&s_end, end);
-                for (int w = 0; w < kPageThreads / 32; ++w) run += part[w];
-                __syncthreads();
+            for (int u = 0; u < kCopies; ++u) {
+                const size_t i = i0 + u * kPageThreads;
+                if (i >= all) break;
+                int p = 0;  // pool i / vecs of the group
+#pragma unroll
+                for (int k = 1; k < kForkPools; ++k) p += i >= k * vecs;
+                char* pool = static_cast<char*>(pools.p[p0 + p]);
+                v[u] = reinterpret_cast<const uint4*>(pool + from)[i - p * vecs];
+                dst[u] = reinterpret_cast<uint4*>(pool + to) + (i - p * vecs);
             }
-            if (threadIdx.x == 0) *a.next_free_out = (int)s_end;
-        }
-    }
-    // the part-filled page: the rows before kv_len go to the child's own page
-    const int tail = c.par >= 0 ? c.kv % a.P : 0;
-    if (tail == 0 || c.first) return;
-    const int src = a.page_table[(size_t)c.par * a.max_pages + c.have];
-    if (src < 0 || src >= a.num_pages) {
-        if (blockIdx.y == 0 && threadIdx.x == 0) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
-        return;
-    }
-    // this CTA's share of the pools as one long list of vectors, kCopies loads in
-    // flight per thread: a page's rows of one pool alone (2 to 30 KB) leave the
-    // memory waiting (72 pools, 45 slots: 17.3 us a pool per CTA, COPY_NEW us so)
-    const unsigned vecs = (unsigned)((size_t)tail * a.row_bytes / 16);
-    const int p0 = (int)((long long)a.n_pools * blockIdx.y / gridDim.y);
-    const int p1 = (int)((long long)a.n_pools * (blockIdx.y + 1) / gridDim.y);
-    const unsigned long long all = (unsigned long long)(p1 - p0) * vecs;
-    for (unsigned long long i0 = threadIdx.x; i0 < all; i0 += kCopies * kPageThreads) {
-        uint4 v[kCopies];
-        uint4* to[kCopies];
 #pragma unroll
-        for (int u = 0; u < kCopies; ++u) {
-            const unsigned long long i = i0 + u * kPageThreads;
-            if (i >= all) break;
-            const unsigned p = all >> 32 ? (unsigned)(i / vecs) : (unsigned)i / vecs, x = (unsigned)(i - (unsigned long long)p * vecs);
-            char* pool = static_cast<char*>(pools.p[p0 + p]);
-            v[u] = reinterpret_cast<const uint4*>(pool + (size_t)src * a.page_bytes)[x];
-            to[u] = reinterpret_cast<uint4*>(pool + (size_t)base * a.page_bytes) + x;
+            for (int u = 0; u < kCopies; ++u)
+                if (i0 + u * kPageThreads < all) *dst[u] = v[u];
         }
-#pragma unroll
-        for (int u = 0; u < kCopies; ++u)
-            if (i0 + u * kPageThreads < all) *to[u] = v[u];
     }
 }
 
@@ -230,28 +231,6 @@ __global__ void __launch_bounds__(kPageThreads) mark_kernel(const __grid_constan
         if (id < 0 || id >= a.num_pages) raise_flag(a.err_flag, ISD_FLAG_PAGE_OOB);
         else atomicOr(&a.live[id >> 5], 1u << (id & 31));
     }
-}
-
-// Exclusive scan over the CTA; returns the total.
-template <int THREADS>
-ISD_DEVINL int block_scan(int v, int& before, int* part) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = v;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += u;
-    }
-    if (lane == 31) part[warp] = incl;
-    __syncthreads();
-    int base = 0, total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) base += part[w];
-        total += part[w];
-    }
-    __syncthreads();
-    before = base + incl - v;
-    return total;
 }
 
 // L pages are in use; the k-th used page at or past L moves to the k-th free
@@ -404,10 +383,10 @@ cudaError_t launch_fork(const isd_dims* d, int R, const int32_t* parent, const i
         PoolList list;
         a.n_pools = n_pools - p0 < kPoolsPerLaunch ? n_pools - p0 : kPoolsPerLaunch;
         for (int i = 0; i < a.n_pools; ++i) list.p[i] = pools[p0 + i];
-        // as many CTAs as run at once (3 an SM): each first works out the slots before its own
-        const int shares = std::max(1, std::min(a.n_pools, 3 * persistent_grid() / R));
-        const cudaError_t e = launch_kernel(false, fork_kernel, dim3(R, shares),
-                                            dim3(kPageThreads), (size_t)d->B * 4, st, a, list);
+        const long long jobs = (long long)R * std::max(1, (a.n_pools + kForkPools - 1) / kForkPools);
+        const int grid = (int)std::min(jobs, 3ll * persistent_grid());  // as many as run at once
+        const cudaError_t e = launch_kernel(false, fork_kernel, dim3(grid), dim3(kPageThreads),
+                                            ((size_t)d->B + R) * 4, st, a, list);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

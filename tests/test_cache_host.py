@@ -147,7 +147,8 @@ def test_fork_refusals(isd):
     assert call(pools=None) == isd.ISD_ERR_INVALID_ARG
     assert call(pools=(ctypes.c_void_p * 2)(1 << 30, None)) == isd.ISD_ERR_INVALID_ARG
     assert call(pools=(ctypes.c_void_p * 2)(1 << 30, (1 << 31) + 8)) == isd.ISD_ERR_INVALID_ARG
-    assert call(dd=_dims(isd, B=12001)) == isd.ISD_ERR_UNSUPPORTED_SHAPE
+    assert call(dd=_dims(isd, B=11998)) == isd.ISD_ERR_UNSUPPORTED_SHAPE
+    assert call(R=11999) == isd.ISD_ERR_UNSUPPORTED_SHAPE
     assert call(dd=_dims(isd, Hkv=1, D=4)) == isd.ISD_ERR_UNSUPPORTED_SHAPE
     bad = _dims(isd)
     bad.num_pages = 0

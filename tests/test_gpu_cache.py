@@ -432,6 +432,12 @@ def test_fork_many(isd):
     check_fork(isd, c, rng.integers(-1, B, R).tolist(), rng.integers(0, 9, R).tolist())
 
 
+def test_fork_as_many_slots_as_go(isd):
+    rng = np.random.default_rng(2)
+    c = Cache(isd, 2000, 2, rng.integers(0, 9, 2000), layers=1, Hkv=1, D=8, spare=30000, seed=3)
+    check_fork(isd, c, rng.integers(-1, 2000, 10000).tolist(), rng.integers(0, 3, 10000).tolist())
+
+
 def test_fork_faults(isd):
     c = Cache(isd, 3, 16, [33, 16, 100], spare=2, seed=3)
     check_fork(isd, c, [0, 7, -2, 1], flags=isd.FLAG_PARENT_OOB)
