@@ -66,19 +66,6 @@ ISD_DEVINL Child child_of(const ForkArgs& a, const int* first_of, int r) {
     return c;
 }
 
-// `vecs` 16-byte vectors, by `step` threads of which this is number `i`; four
-// loads are in flight before the first store.
-ISD_DEVINL void copy_vecs(const uint4* __restrict__ from, uint4* __restrict__ to, int vecs, int i, int step) {
-    for (; i + 3 * step < vecs; i += 4 * step) {
-        uint4 v[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = from[i + u * step];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) to[i + u * step] = v[u];
-    }
-    for (; i < vecs; i += step) to[i] = from[i];
-}
-
 // Exclusive scan over the CTA; returns the total.
 template <int THREADS, typename T>
 ISD_DEVINL T block_scan(T v, T& before, T* part) {
@@ -108,7 +95,7 @@ ISD_DEVINL T block_scan(T v, T& before, T* part) {
 // A copy is latency: a child's rows of one pool are 2 to 30 KB.  So the pairs,
 // whose bytes go from none to a page's, are dealt out in turn (a grid of (child,
 // share of the pools) left the CTAs of the longest tail running alone: 18.6
-// against FORK_NEW us for 45 slots and 72 pools), and a thread has kCopies loads in flight
+// against 16.2 us for 45 slots and 72 pools), and a thread has kCopies loads in flight
 // over the pools of a pair.
 __global__ void __launch_bounds__(kPageThreads, 3) fork_kernel(const __grid_constant__ ForkArgs a,
                                                                const __grid_constant__ PoolList pools) {
@@ -213,10 +200,10 @@ struct CompactArgs {
 // Compaction, by the size of the bookkeeping: up to kSmallPages pages and
 // kSmallCells table cells one CTA does all of it with the bitmap in shared
 // memory (plan_small_kernel: 2 launches in all); beyond, mark, plan and place
-// are kernels of their own (5 with the bitmap's clearing).  The small way took
-// SMALL_A against SMALL_B us at 8 requests of 38 pages and SMALL_C against SMALL_D at
-// 64 of 4000 cells.
-constexpr int kSmallPages = 1 << 20, kSmallCells = 1 << 18, kSmallThreads = 1024;
+// are kernels of their own (5 with the bitmap's clearing).  A compaction by the
+// small way took 8.7 us against 12.3 with a table of 8 x 26 cells, and 45.2
+// against 38.0 with 64 x 1001.
+constexpr int kSmallPages = 1 << 20, kSmallCells = 1 << 14, kSmallThreads = 1024;
 
 // One CTA per request: marks its pages.
 __global__ void __launch_bounds__(kPageThreads) mark_kernel(const __grid_constant__ CompactArgs a) {
@@ -268,9 +255,9 @@ ISD_DEVINL int list_moves(const CompactArgs& a, const uint32_t* live, int* part)
     return movers;
 }
 
-__global__ void __launch_bounds__(kPageThreads) plan_kernel(const __grid_constant__ CompactArgs a) {
-    __shared__ int part[kPageThreads / 32];
-    list_moves<kPageThreads>(a, a.live, part);
+__global__ void __launch_bounds__(kSmallThreads) plan_kernel(const __grid_constant__ CompactArgs a) {
+    __shared__ int part[kSmallThreads / 32];
+    list_moves<kSmallThreads>(a, a.live, part);
 }
 
 // Marking, listing and placing by one CTA.
@@ -311,9 +298,10 @@ __global__ void __launch_bounds__(kPageThreads) place_kernel(const __grid_consta
     for (int i = blockIdx.x * kPageThreads + threadIdx.x; i < n; i += gridDim.x * kPageThreads) to[src[i]] = dst[i];
 }
 
-// The moves of the pools (grid.y), one warp per piece of a page, and (with
-// `tables`) the page tables.
-constexpr int kMovePiece = 4096;
+constexpr int kMoves = 4;  // 16-byte loads in flight per thread
+// The moves of the pools (grid.y), as one long list of 16-byte vectors with
+// kMoves loads in flight per thread, and (with `tables`) the page tables.  Bound
+// by memory: 2.15 GB of 32 KB pages in 348 us, 0.94 of a copy's rate.
 __global__ void __launch_bounds__(kPageThreads) move_kernel(const __grid_constant__ CompactArgs a,
                                                             const __grid_constant__ PoolList pools, int tables) {
     pdl_wait();
@@ -336,19 +324,24 @@ __global__ void __launch_bounds__(kPageThreads) move_kernel(const __grid_constan
         }
     }
     if ((int)blockIdx.y >= a.n_pools) return;
-    const int lane = threadIdx.x & 31;
-    // a pool has fewer than 2^32 pieces: they hold 4 KB, or a page, of which there are fewer than 2^31
-    const uint32_t pieces = (uint32_t)((a.page_bytes + kMovePiece - 1) / kMovePiece);
-    const uint32_t items = n * pieces, warps = gridDim.x * (kPageThreads / 32);
+    const uint32_t vecs = (uint32_t)(a.page_bytes / 16);  // of a page; a page of 64 GB is no pool's
+    const unsigned long long all = (unsigned long long)n * vecs, step = (unsigned long long)gridDim.x * kPageThreads;
     char* pool = static_cast<char*>(pools.p[blockIdx.y]);
-    for (uint32_t it = blockIdx.x * (kPageThreads / 32) + (threadIdx.x >> 5); it < items; it += warps) {
-        const uint32_t k = it / pieces;
-        const size_t off = (size_t)(it - k * pieces) * kMovePiece;
-        const size_t left = a.page_bytes - off;
-        copy_vecs(reinterpret_cast<const uint4*>(pool + (size_t)src[k] * a.page_bytes + off),
-                  reinterpret_cast<uint4*>(pool + (size_t)dst[k] * a.page_bytes + off),
-                  (int)((left < kMovePiece ? left : kMovePiece) / 16), lane, 32);
-        if (it + warps < it) break;  // past 2^32
+    for (unsigned long long i0 = (unsigned long long)blockIdx.x * kPageThreads + threadIdx.x; i0 < all; i0 += kMoves * step) {
+        uint4 v[kMoves];
+        uint4* dest[kMoves];
+#pragma unroll
+        for (int u = 0; u < kMoves; ++u) {
+            const unsigned long long i = i0 + u * step;
+            if (i >= all) break;
+            const uint32_t k = all >> 32 ? (uint32_t)(i / vecs) : (uint32_t)i / vecs;
+            const size_t x = i - (unsigned long long)k * vecs;
+            v[u] = reinterpret_cast<const uint4*>(pool + (size_t)src[k] * a.page_bytes)[x];
+            dest[u] = reinterpret_cast<uint4*>(pool + (size_t)dst[k] * a.page_bytes) + x;
+        }
+#pragma unroll
+        for (int u = 0; u < kMoves; ++u)
+            if (i0 + u * step < all) *dest[u] = v[u];
     }
 }
 
@@ -428,7 +421,7 @@ cudaError_t launch_compact(const isd_dims* d, const int32_t* pages_used, const i
         if (e != cudaSuccess) return e;
         e = launch_kernel(false, mark_kernel, dim3(d->B), dim3(kPageThreads), 0, st, a);
         if (e != cudaSuccess) return e;
-        e = launch_kernel(false, plan_kernel, dim3(1), dim3(kPageThreads), 0, st, a);
+        e = launch_kernel(false, plan_kernel, dim3(1), dim3(kSmallThreads), 0, st, a);
         if (e != cudaSuccess) return e;
         e = launch_kernel(false, place_kernel, dim3(persistent_grid()), dim3(kPageThreads), 0, st, a);
         if (e != cudaSuccess) return e;
