@@ -1358,11 +1358,28 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     }
 }
 
+// Running maximum, sum and weighted values of a row: another part joins them.
+template <int N>
+ISD_DEVINL void join_part(float& m, float& l, float (&o)[N], float mk, float lk, const float (&ok)[N]) {
+    const float mn = fmaxf(m, mk), mu = mn == -INFINITY ? 0.f : mn;
+    const float f0 = ex2(m - mu), f1 = ex2(mk - mu);
+    l = l * f0 + lk * f1;
+#pragma unroll
+    for (int e = 0; e < N; ++e)  // a part of no weight counts for nothing
+        o[e] = (f0 > 0.f ? o[e] * f0 : 0.f) + (f1 > 0.f ? ok[e] * f1 : 0.f);
+    m = mn;
+}
+
 // Joins the parts of cut items, always in the same order: grid (CTAs, 32-row
-// groups, slices of the dimensions), a lane per row.  `share` warps take the parts
-// in turn, for 16 dimensions; the groups of such warps take other dimensions.
-// They meet in shared memory.
-constexpr int kJoinWarps = 8, kJoinDims = 16;
+// groups, slices of the dimensions), a lane per row.  Of few parts a warp joins
+// D / 8 dimensions, the loads of two parts in flight.  Of more (a long context)
+// `share` warps take the parts in turn, for 16 dimensions, and meet in shared
+// memory.  With many rows the blocks hide each other's loads, so the first way
+// holds up to kJoinMany parts: 2048 tokens at once took 8 us of the call against
+// 12 by the second way, prompts of 3 to 333 tokens with 64-wide heads 5 against
+// 12.  With few rows it holds up to kJoinFew: one token behind 1000 took 3.4 us by
+// the second way against 5 by the first.
+constexpr int kJoinWarps = 8, kJoinDims = 16, kJoinFew = 3, kJoinMany = 16;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
     __shared__ float red[kJoinWarps][kJoinDims + 2][32];
@@ -1374,38 +1391,60 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
     const int i = cut.i0 + row / kTileRows * a.tpq + rr / a.grp;
     const bool live = rr < a.tpq * a.grp && i < cut.i1;
     if (!__any_sync(0xffffffffu, live)) return;  // the same lanes in every warp
-    const int share = cut.parts >= 8 ? 8 : cut.parts >= 4 ? 4 : 2, mine = warp % share;
-    const int span = kJoinDims * (kJoinWarps / share);  // dimensions at once
     const size_t stride = (size_t)a.part_rows * (D + 2);
     const float* first = a.part + ((size_t)blockIdx.x * 2 + 1) * stride;
+    // part k: the first one in slot 1 of its CTA, the others in slot 0 of theirs
+    auto part = [&](int k) { return k == 0 ? first : first + (size_t)(2 * k - 1) * stride; };
+    auto load = [&](const float* pk, int d, float* to, int count) {
+        const float4* po = reinterpret_cast<const float4*>(pk + 2 * a.part_rows) + (size_t)(d / 4) * a.part_rows + row;
+#pragma unroll
+        for (int e = 0; e < count; e += 4) {
+            const float4 v = po[(size_t)(e / 4) * a.part_rows];
+            to[e] = v.x;
+            to[e + 1] = v.y;
+            to[e + 2] = v.z;
+            to[e + 3] = v.w;
+        }
+    };
     __nv_bfloat16* out = a.out + ((size_t)(cut.start + i) * a.Hq + cut.g * a.grp + rr % a.grp) * D;
+    if (cut.parts <= (a.part_rows > kTileRows ? kJoinMany : kJoinFew)) {
+        if (!live || blockIdx.z) return;
+        constexpr int N = D / kJoinWarps, kBatch = 2;
+        const int d0 = warp * N;
+        float m = -INFINITY, l = 0.f, o[N] = {};
+        for (int k0 = 0; k0 < cut.parts; k0 += kBatch) {
+            float mk[kBatch], lk[kBatch], ok[kBatch][N];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (k0 + j >= cut.parts) continue;
+                const float* pk = part(k0 + j);
+                mk[j] = pk[row];
+                lk[j] = pk[a.part_rows + row];
+                load(pk, d0, ok[j], N);
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (k0 + j < cut.parts) join_part(m, l, o, mk[j], lk[j], ok[j]);
+        }
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int e = 0; e < N; e += 8)
+            *reinterpret_cast<uint4*>(out + d0 + e) =
+                make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                           pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+        return;
+    }
+    const int share = cut.parts >= 8 ? 8 : 4, mine = warp % share;
+    const int span = kJoinDims * (kJoinWarps / share);  // dimensions at once
     for (int base = blockIdx.z * span; base < D; base += gridDim.z * span) {
         const int d0 = base + warp / share * kJoinDims;
-        float m = -INFINITY, l = 0.f, o[kJoinDims];
-#pragma unroll
-        for (int e = 0; e < kJoinDims; ++e) o[e] = 0.f;
+        float m = -INFINITY, l = 0.f, o[kJoinDims] = {};
         if (live && d0 < D) {
             for (int k = mine; k < cut.parts; k += share) {
-                // part k: the first one in slot 1 of its CTA, the others in slot 0 of theirs
-                const float* pk = k == 0 ? first : first + (size_t)(2 * k - 1) * stride;
-                const float4* po = reinterpret_cast<const float4*>(pk + 2 * a.part_rows) + (size_t)(d0 / 4) * a.part_rows + row;
-                const float mk = pk[row], lk = pk[a.part_rows + row];
+                const float* pk = part(k);
                 float ok[kJoinDims];
-#pragma unroll
-                for (int e = 0; e < kJoinDims; e += 4) {
-                    const float4 v = po[(size_t)(e / 4) * a.part_rows];
-                    ok[e] = v.x;
-                    ok[e + 1] = v.y;
-                    ok[e + 2] = v.z;
-                    ok[e + 3] = v.w;
-                }
-                const float mn = fmaxf(m, mk), mu = mn == -INFINITY ? 0.f : mn;
-                const float f0 = ex2(m - mu), f1 = ex2(mk - mu);
-                l = l * f0 + lk * f1;
-#pragma unroll
-                for (int e = 0; e < kJoinDims; ++e)  // a part of no weight counts for nothing
-                    o[e] = (f0 > 0.f ? o[e] * f0 : 0.f) + (f1 > 0.f ? ok[e] * f1 : 0.f);
-                m = mn;
+                load(pk, d0, ok, kJoinDims);
+                join_part(m, l, o, pk[row], pk[a.part_rows + row], ok);
             }
         }
         red[warp][0][lane] = m;
@@ -1426,11 +1465,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
             if (w < share) sum += f[w] * red[w0 + w][1][lane];
         }
         const float inv = 1.f / sum;
-        const int per = kJoinDims / share;  // 8, 4 or 2
+        const int per = kJoinDims / share;  // 4 or 2
         if (live && d0 < D) {
-            uint32_t h[4];
+            uint32_t h[2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 if (2 * q >= per) break;
                 float x = 0.f, y = 0.f;
 #pragma unroll
@@ -1442,8 +1481,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
                 h[q] = pack_bf16(x * inv, y * inv);
             }
             __nv_bfloat16* to = out + d0 + mine * per;
-            if (per == 8) *reinterpret_cast<uint4*>(to) = make_uint4(h[0], h[1], h[2], h[3]);
-            else if (per == 4) *reinterpret_cast<uint2*>(to) = make_uint2(h[0], h[1]);
+            if (per == 4) *reinterpret_cast<uint2*>(to) = make_uint2(h[0], h[1]);
             else *reinterpret_cast<uint32_t*>(to) = h[0];
         }
         __syncthreads();
@@ -1514,8 +1552,8 @@ cudaError_t launch_chunk_d(const ChunkArgs& a, const uint16_t* q, cudaStream_t s
     e = launch_kernel(false, chunk_kernel<D>, dim3(grid), dim3(kChunkThreads), ChunkShape<D>::kSmem(), st, tq, tqs, tk,
                       tv, tkn, tvn, a);
     if (e != cudaSuccess) return e;
-    // 8 to 16 blocks per CTA of the cut, whatever the rows
-    const int groups = a.part_rows / 32, slices = groups >= 8 ? 2 : groups >= 4 ? 4 : D / kJoinDims;
+    // about 8 blocks per CTA of the cut, whatever the rows
+    const int groups = a.part_rows / 32, slices = groups >= 8 ? 1 : groups >= 4 ? 4 : D / kJoinDims;
     return launch_kernel(true, chunk_join_kernel<D>, dim3(grid, groups, slices), dim3(32 * kJoinWarps), 0, st, a);
 }
 
