@@ -358,7 +358,6 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         sh->bad_piece = -1;
         sh->b = a.B;
         fence_mbar_init();
-        a.cuts[blockIdx.x].parts = 0;
     }
     if (warp == 9 && lane == 0) {
         prefetch_tmap(&tm_q);
@@ -372,6 +371,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         tmem_alloc(&sh->tmem, kTmemCols);
         tmem_relinquish();
     }
+    // what comes before in the stream is done from here on (nothing global was
+    // touched so far: the previous call's joining kernel may still read `cuts`)
+    pdl_wait();
+    if (threadIdx.x == 0) a.cuts[blockIdx.x].parts = 0;
     bool bad = false;
     {
         // costs of the requests, summed in order: a thread per request, and
@@ -1383,7 +1386,7 @@ constexpr int kJoinWarps = 8, kJoinDims = 16, kJoinFew = 3, kJoinMany = 16;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
     __shared__ float red[kJoinWarps][kJoinDims + 2][32];
-    pdl_wait();
+    pdl_wait();  // (and no early trigger: the next call's CTAs among these cost 2 to 6% with many rows)
     const ChunkCut cut = a.cuts[blockIdx.x];
     if (cut.parts < 2) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1549,7 +1552,9 @@ cudaError_t launch_chunk_d(const ChunkArgs& a, const uint16_t* q, cudaStream_t s
         return cudaErrorInvalidValue;
     }
     const int grid = persistent_grid();
-    e = launch_kernel(false, chunk_kernel<D>, dim3(grid), dim3(kChunkThreads), ChunkShape<D>::kSmem(), st, tq, tqs, tk,
+    // its launch, barriers and TMEM go under the end of the kernel before it (18.5 to
+    // 16.6 us a call for one token behind 1000, call after call)
+    e = launch_kernel(true, chunk_kernel<D>, dim3(grid), dim3(kChunkThreads), ChunkShape<D>::kSmem(), st, tq, tqs, tk,
                       tv, tkn, tvn, a);
     if (e != cudaSuccess) return e;
     // about 8 blocks per CTA of the cut, whatever the rows
