@@ -761,6 +761,11 @@ isd_status isd_chunk_attention(const isd_dims* d, int32_t T, const uint16_t* q,
     if (overlaps(out, out_n, q, out_n) || overlaps(out, out_n, k_new, new_n) || overlaps(out, out_n, v_new, new_n) ||
         overlaps(out, out_n, k_pool, pool_n) || overlaps(out, out_n, v_pool, pool_n))
         return invalid("out overlaps an input");
+    if (overlaps(k_pool, pool_n, v_pool, pool_n) || overlaps(k_new, new_n, k_pool, pool_n) ||
+        overlaps(k_new, new_n, v_pool, pool_n) || overlaps(v_new, new_n, k_pool, pool_n) ||
+        overlaps(v_new, new_n, v_pool, pool_n) || overlaps(q, out_n, k_pool, pool_n) ||
+        overlaps(q, out_n, v_pool, pool_n))
+        return invalid("a pool overlaps the other one or an input");
     ISD_CUDA(isd::launch_chunk_attention(d, T, q, k_new, v_new, k_pool, v_pool, page_table, kv_len,
                                          q_start, out, ws, err_flag, static_cast<cudaStream_t>(stream)));
     return ISD_OK;

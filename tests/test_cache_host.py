@@ -117,6 +117,10 @@ def test_chunk_refusals(isd):
     p = [at(k) for k in range(9)]
     p[8] = ctypes.c_void_p(p[4].value + d.num_pages * d.page_size * 2 * 128 * 2 - 16)
     assert call(p=p) == isd.ISD_ERR_INVALID_ARG
+    for i, j in ((3, 4), (0, 3), (1, 3), (1, 4), (2, 3), (2, 4), (0, 4)):
+        p = [at(k) for k in range(9)]
+        p[i] = ctypes.c_void_p(p[j].value + 32)
+        assert call(p=p) == isd.ISD_ERR_INVALID_ARG, (i, j)
     # no rows: nothing to do, and nothing is launched
     assert call(T=0) == isd.ISD_OK
 

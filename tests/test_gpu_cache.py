@@ -354,6 +354,59 @@ def test_chunk_call_object_and_larger_workspace(isd):
     c.check()
 
 
+def test_chunk_no_rows(isd):
+    c = Chunk(isd, 4, 2, 128, 16, [10, 30], [0, 0], seed=16).upload()
+    keep = [p.clone() for p in c.d_pool]
+    c.call()
+    torch.cuda.synchronize()
+    assert int(c.err.item()) == 0
+    for p, k in zip(c.d_pool, keep):
+        assert torch.equal(p.view(torch.int16), k.view(torch.int16))
+
+
+@pytest.mark.parametrize("P", [16, 20])
+def test_far_pages(isd, P):
+    """Pages past 2^32 bytes and 2^31 elements of a pool: the same results as in
+    a small one, for all three operators."""
+    Hq, Hkv, D, cols, far = 8, 2, 128, 20, 5_800_000_000 // (P * 2 * 128 * 2)
+    ctx, n = [150, 37, 0], [40, 1, 70]
+    used = [-(-(c + m) // P) for c, m in zip(ctx, n)]
+    small = 2 * sum(used) + 8
+    rng = np.random.default_rng(P)
+    q, k, v = bf16(rng, 111, Hq, D).cuda(), bf16(rng, 111, Hkv, D).cuda(), bf16(rng, 111, Hkv, D).cuda()
+    data = [bf16(rng, small, P, Hkv, D).cuda() for _ in range(2)]
+    ids = rng.permutation(sum(used)) + small // 3
+    got = []
+    for shift in (0, far - small):
+        pages = small + shift
+        pools = [torch.empty(pages, P, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        for p, x in zip(pools, data):
+            p[shift:] = x
+        table = np.full((3, cols), -1, np.int32)
+        at = 0
+        for b, u in enumerate(used):
+            table[b, :u] = ids[at:at + u] + shift
+            at += u
+        d = isd.make_dims(3, 1, Hq, Hkv, D, 1, P, pages, cols)
+        out, err = torch.empty(111, Hq * D, dtype=torch.bfloat16, device="cuda"), i32([0])
+        isd.chunk_attention(d, q, k, v, *pools, i32(table), i32(ctx), i32(np.cumsum([0] + n)), out,
+                            isd.alloc_chunk_workspace(d, 111), err)
+        kv, us = i32([c + m for c, m in zip(ctx, n)]), i32(used)
+        new = [i32([0] * 2), i32([0] * 2), torch.empty(2, cols, dtype=torch.int32, device="cuda"), i32([0])]
+        isd.fork_requests(d, i32([0, 0]), kv, us, i32(table), i32([pages - 4]), pools, *new, err_flag=err)
+        tail = [p[new[2][1, new[0][1].item() // P].item(), :new[0][1].item() % P].clone() for p in pools]
+        d2 = isd.make_dims(2, 1, Hq, Hkv, D, 1, P, pages, cols)
+        isd.compact_pages(d2, new[2], new[1], pools, new[2], new[3], isd.alloc_pages_workspace(d2), err_flag=err)
+        rows = [torch.cat([p[j] for j in new[2][r, :new[1][r].item()].tolist()])[:new[0][r].item()]
+                for p in pools for r in range(2)]
+        assert int(err.item()) == 0
+        got.append([out, *tail, *rows, new[3]])
+        del pools
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert got[0][-1].item() < small
+
+
 def test_chunk_refuses_wrong_tensors(isd):
     c = Chunk(isd, 4, 2, 128, 16, [10], [4], seed=16).upload()
     with pytest.raises(ValueError):
