@@ -1093,8 +1093,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 if (t >= p.kvt) return i + 1 - (t - p.kvt) * kKeys;
                 return p.kv - t * kKeys + (p.merged && t == p.kvt - 1 ? i + 1 : 0);
             };
-            // Weights are taken by the reference as it is.  Only when a row's sum of
-            // them passes 2^10 (then one may be large), or is none, is its maximum
+            // Weights are taken by the reference as it is.  Only when there is none yet,
+            // or a row's sum of them passes 2^10 (then one may be large) or is NaN, is its maximum
             // looked up, the reference moved, and the weights are done over: S is
             // still there.
             if (quad) {
@@ -1106,7 +1106,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     tmem_ld32(tm_s + wq * 32, s);
                     tmem_arrived(s);
                     hide(s, partly(t), seen_of(t) - wq * 32);
-                    if (!has_o) move_ref(top_of(s) * a.scale_log2, false);
+                    // a row's first scores set its reference (a quarter may have seen none so far)
+                    if (__any_sync(0xffffffffu, live && m_ref == -INFINITY)) move_ref(top_of(s) * a.scale_log2, has_o);
                     uint32_t w[16];
                     float sum;
 #pragma unroll 1
@@ -1163,7 +1164,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                             if (h == 0) tmem_ld32(tm_s + 64, s0);
                             weights(s1, mu, acc, w + 16);
                             const float sum = sum_of(acc);
-                            if (__builtin_expect(__any_sync(0xffffffffu, live && !(sum <= 1024.f)), 0)) {
+                            if (__builtin_expect(__any_sync(0xffffffffu, live && (!(sum <= 1024.f) || m_ref == -INFINITY)), 0)) {
                                 if (h == 0) tmem_arrived(s0);
                                 break;
                             }

@@ -133,6 +133,8 @@ SHAPES = {
     "group_8": (64, 8, 128, 16, [130, 1], [20, 1]),
     "group_128": (128, 1, 128, 16, [130, 7], [3, 1]),
     "group_100": (100, 1, 64, 16, [140, 0], [3, 2]),
+    "remainders": (5, 1, 128, 16, [36, 52, 40, 37], [255, 303, 204, 302]),
+    "remainders_d64": (3, 1, 64, 8, [20, 70, 100], [258, 513, 389]),
     "split_rows": (8, 2, 128, 16, [9000], [70]),
     "many_requests": (4, 2, 128, 16, [(37 * i) % 300 for i in range(90)], [(5 * i) % 4 for i in range(90)]),
 }
@@ -257,6 +259,31 @@ def test_chunk_repeats_bit_for_bit(isd):
         c.call()
         torch.cuda.synchronize()
         assert torch.equal(c.out.view(torch.int16), first.view(torch.int16))
+
+
+@pytest.mark.parametrize("n", [1, 2, 40, 90])
+@pytest.mark.parametrize("first", [100, 200, 390])
+def test_chunk_first_scores_are_minus_infinity(isd, n, first):
+    """Keys of score -inf count for nothing, also where they are a row's first
+    tiles: the rows are the attention over the keys after them."""
+    B, kv = 12, 400
+    c = Chunk(isd, 8, 8, 128, 16, [kv] * B, [n] * B, seed=first + n)
+    c.q[:] = c.q.abs() + 0.125
+    pos = np.arange(kv)
+    for b in range(B):
+        c.k_pool[c.table[b, pos[:first] // 16], pos[:first] % 16] = float("-inf")
+    c.upload().call()
+    torch.cuda.synchronize()
+    assert int(c.err.item()) == 0
+    kp = O.append(f64(c.k_pool), f64(c.k_new), c.table, c.ctx, c.start)
+    vp = O.append(f64(c.v_pool), f64(c.v_new), c.table, c.ctx, c.start)
+    got = f64(c.out).reshape(-1, 8, 128)
+    for b in range(B):
+        k, v = (O.rows_of(x, c.table[b], kv + n)[first:] for x in (kp, vp))
+        q = f64(c.q)[c.start[b]:c.start[b + 1]]
+        want = O.chunk_attention(q, k[:, None], v[:, None], [list(range(kv + n - first))], [kv - first], [0, n],
+                                 c.dims.sm_scale)
+        check_rows(got[c.start[b]:c.start[b + 1]], *want, 128, kv + n)
 
 
 def test_chunk_in_pieces_is_the_whole(isd):
