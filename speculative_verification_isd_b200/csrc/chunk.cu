@@ -1115,7 +1115,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         unsigned long long acc = 0;
                         weights(s, mu_of(), acc, w);
                         sum = sum_of(acc);
-                        if (__builtin_expect(round || !__any_sync(0xffffffffu, sum > 1024.f), 1)) break;
+                        if (__builtin_expect(round || !__any_sync(0xffffffffu, live && sum > 1024.f), 1)) break;
                         move_ref(top_of(s) * a.scale_log2, has_o);
                     }
                     l += sum;
@@ -1144,7 +1144,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                             top = fmaxf(top, top_of(s0));
                         }
                         top *= a.scale_log2;
-                        if (__any_sync(0xffffffffu, top > m_ref + over)) move_ref(top, has_o);
+                        // (rows that are no one's have whatever is in Q: they decide nothing)
+                        if (__any_sync(0xffffffffu, live && top > m_ref + over)) move_ref(top, has_o);
                     };
                     if (__builtin_expect(!has_o || some, 0)) look(0, kKeys, has_o ? 8.f : 0.f, has_o);
                     // half by half; P takes the place of scores already read

@@ -251,10 +251,17 @@ def test_chunk_opposite_infinities(isd):
     c.upload().call().check()
 
 
-def test_chunk_repeats_bit_for_bit(isd):
-    c = Chunk(isd, 8, 2, 128, 16, [5000, 10, 300], [30, 200, 1], seed=6).upload().call()
+@pytest.mark.parametrize("heads,ctx,n", [((8, 2, 128), [5000, 10, 300], [30, 200, 1]),
+                                         ((28, 4, 128), [(701 * i) % 3000 for i in range(20)],
+                                          [1 + (7 * i) % 40 for i in range(20)])])
+def test_chunk_repeats_bit_for_bit(isd, heads, ctx, n):
+    """Also where rows of a tile are no one's, whatever other calls left behind
+    on the chip meanwhile."""
+    c = Chunk(isd, *heads, 16, ctx, n, seed=6).upload().call()
+    other = Chunk(isd, *heads, 16, [900] * 6, [70, 3, 20, 1, 9, 130], seed=7, gain=30.0).upload()
     first = c.out.clone()
-    for _ in range(3):
+    for _ in range(4):
+        other.call()
         c.out.fill_(3.0)
         c.call()
         torch.cuda.synchronize()
