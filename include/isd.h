@@ -544,8 +544,8 @@ isd_status isd_layers(const isd_dims* d, int32_t n_layers, int32_t inter, float 
  * ISD_ERR_WORKSPACE.  On the device: ISD_FLAG_CHUNK_RANGE (no request is
  * served); ISD_FLAG_CAPACITY (a request with a negative kv_len or tokens past
  * its pages or 2^30: its rows of out are zero, its cache is left alone);
- * ISD_FLAG_PAGE_OOB (keys and values on a page id outside the pool read as
- * zeros, and are not written).  Two calls may overlap on the GPU if their
+ * ISD_FLAG_PAGE_OOB (keys and values on a page id outside the pool, cached or
+ * new, read as zeros, and are not written).  Two calls may overlap on the GPU if their
  * workspaces and the cache rows they write differ.
  */
 size_t isd_chunk_workspace_bytes(const isd_dims* d, int32_t T);

@@ -200,7 +200,9 @@ struct ChunkShared {
     uint32_t issued[2];  // K, V tiles that their producer has begun to load
     uint32_t appended;   // new tokens taken for appending
     uint32_t fixed;      // pieces that the fixing warp is done with
+    uint32_t checked;    // pieces whose `holed` it has set
     uint32_t epilogues[2];  // finished by the warps of a softmax warpgroup (4 a piece)
+    int holed[kPieces];  // whether the fixing warp touches every tile of new tokens of a piece
     int bad_piece;       // the piece whose `bad_from` holds, or -1
     int bad_from[3][D];  // first new token with +inf, -inf, NaN in dimension d of V
 };
@@ -361,7 +363,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         mbar_init(&sh->meet, 8);
         mbar_init(&sh->drain, 1);
         sh->abort_flag = sh->never = 0;
-        sh->published = sh->issued[0] = sh->issued[1] = sh->appended = sh->fixed = sh->epilogues[0] = sh->epilogues[1] = 0;
+        sh->published = sh->issued[0] = sh->issued[1] = sh->appended = sh->fixed = sh->checked = sh->epilogues[0] = sh->epilogues[1] = 0;
         sh->bad_piece = -1;
         sh->b = a.B;
         fence_mbar_init();
@@ -614,19 +616,21 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     return true;
                 };
                 Piece p;
-                for (uint32_t n = 0; ok && __all_sync(0xffffffffu, piece_at(n, p)); ++n) {
+                for (uint32_t n = 0; ok && __all_sync(0xffffffffu, until(&sh->checked, n + 1) && piece_at(n, p)); ++n) {
                     const int nt = p.t1 - p.t0;
                     const int kvk = p.kvt - p.t0;  // cached tiles ahead
                     auto grouped = [&](int k) { return a.grouped && k < kvk; };
                     // which tiles the fixing warp touches first
                     const int k_fix = p.merged ? kvk - 1 : -1, v_fix = p.kv % kKeys ? kvk - 1 : -1;
-                    const int new_fix = kvk + (p.i0 + 1) / kKeys;
+                    const int holed = *(volatile int*)&sh->holed[n % kPieces] ? kvk : nt;
+                    const int new_fix = min(holed, kvk + (p.i0 + 1) / kKeys);
+                    auto k_fixed = [&](int k) { return k == k_fix || k >= holed; };
                     auto v_fixed = [&](int k) { return k == v_fix || k >= new_fix; };
                     uint32_t ks, vs;
                     // S(k + ...) overwrites P(k), which the product issued before it
                     // reads: the tensor core takes them in this order
                     if (p.mode == kTwo) {
-                        if (!wait_q(0) || !wait_q(1) || !take(kc, false, k_fix == 0, ks)) break;
+                        if (!wait_q(0) || !wait_q(1) || !take(kc, false, k_fixed(0), ks)) break;
                         s_product(0, 0, ks, grouped(0));
                         s_product(1, 1, ks, grouped(0));
                         free_stage(ks);
@@ -634,7 +638,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll 1
                         for (int k = 0; k < nt; ++k) {
                             const bool more = k + 1 < nt;
-                            if (!take(vc, true, v_fixed(k), vs) || (more && !take(kc, false, k + 1 == k_fix, ks))) break;
+                            if (!take(vc, true, v_fixed(k), vs) || (more && !take(kc, false, k_fixed(k + 1), ks))) break;
 #pragma unroll 1
                             for (int w = 0; w < 2; ++w) {
                                 if (!pv_product(w, vs, grouped(k), k == 0)) break;
@@ -651,7 +655,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         const int qs = ones++ & 1;
                         auto s_next = [&](int k) {
                             if (k >= nt) return true;
-                            if (!take(kc, false, k == k_fix, ks)) return false;
+                            if (!take(kc, false, k_fixed(k), ks)) return false;
                             s_product(k & 1, qs, ks, grouped(k));
                             free_stage(ks);
                             return true;
@@ -858,7 +862,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             // are zeroed in V (0 * NaN would spoil the sum), the new tokens of a
             // merged tile are put into their rows, and infinities and NaN in V
             // rows that only some of the item's rows see are taken out and noted
-            // for the epilogue.
+            // for the epilogue.  What a page outside the pool would hold counts as
+            // zeros, new or cached: where a request has new tokens on one, their
+            // rows are zeroed in all its tiles of new tokens.
             uint32_t tiles = 0, n = 0;  // key tiles of the pieces before; pieces
             bool ok = true, more_new = true;
             auto all_ok = [&](bool good) {
@@ -914,8 +920,27 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 __syncwarp();
                 return true;
             };
+            auto outside = [&](int page) { return page < 0 || page >= a.num_pages; };
+            int new_b = -1, new_n = 0;  // whether some of request new_b's first new_n new
+            bool holes = false;         // tokens lie on a page outside the pool
             Piece p;
             while (all_ok(piece_at(n, p))) {
+                const int32_t* table = a.page_table + (size_t)p.b * a.max_pages;
+                if (p.t1 > p.kvt && (p.b != new_b || p.i1 > new_n)) {
+                    if (p.b != new_b) new_n = holes = 0;
+                    const int to = (p.kv + p.i1 - 1) / a.P;
+#pragma unroll 8
+                    for (int c = (p.kv + new_n) / a.P + lane; c <= to; c += 32) holes |= outside(__ldg(table + c));
+                    holes = __any_sync(0xffffffffu, holes);
+                    new_b = p.b;
+                    new_n = p.i1;
+                }
+                const bool holed = p.t1 > p.kvt && holes;
+                if (lane == 0) {
+                    *(volatile int*)&sh->holed[n % kPieces] = holed;
+                    __threadfence_block();
+                    *(volatile uint32_t*)&sh->checked = n + 1;
+                }
                 // the cached tile with free rows, and the new tiles that some row does not see whole
                 if (p.kv % kKeys && p.t0 < p.kvt && p.t1 >= p.kvt) {
                     const uint32_t tile = tiles + (p.kvt - 1 - p.t0);
@@ -923,20 +948,24 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     const int m = p.kv % kKeys;  // cached keys of the tile
                     // the item's new tokens (a row of an item sees none past its last)
                     const int fresh = p.merged ? p.i1 : 0;
+                    uint32_t zeros = 0;  // bit i: token i lies on a page outside the pool
+                    auto new_chunk = [&](const __nv_bfloat16* src, int i) {
+                        if (zeros >> i & 1) return make_uint4(0, 0, 0, 0);
+                        return __ldg(reinterpret_cast<const uint4*>(src + ((size_t)(p.start + i) * a.Hkv + p.g) * D) + ch);
+                    };
                     if (fresh) {
+                        int id = 0;
+                        if (lane < fresh) id = __ldg(table + (p.kv + lane) / a.P);
                         if (!landed(0, tile)) break;
-                        for (int i = r_in; i < fresh; i += kRowsStep)
-                            *cell(ks, m + i, a.grouped) = __ldg(
-                                reinterpret_cast<const uint4*>(a.k_new + ((size_t)(p.start + i) * a.Hkv + p.g) * D) + ch);
+                        zeros = __ballot_sync(0xffffffffu, outside(id));
+                        for (int i = r_in; i < fresh; i += kRowsStep) *cell(ks, m + i, a.grouped) = new_chunk(a.k_new, i);
                         done(ks);
                     }
                     if (!landed(1, tile)) break;
                     for (int i0 = 0; i0 < fresh; i0 += kRowsStep) {
                         const int i = i0 + r_in;
                         uint4 w = make_uint4(0, 0, 0, 0);
-                        if (i < fresh)
-                            w = __ldg(reinterpret_cast<const uint4*>(
-                                          a.v_new + ((size_t)(p.start + i) * a.Hkv + p.g) * D) + ch);
+                        if (i < fresh) w = new_chunk(a.v_new, i);
                         const bool odd = odd_bits(w) & kOddBits;
                         if (__any_sync(0xffffffffu, odd)) {
                             if (!claim()) break;
@@ -949,13 +978,30 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         *cell(vs, row, a.grouped) = make_uint4(0, 0, 0, 0);
                     done(vs);
                 }
-                const int first = max(p.t0, p.kvt + p.i0 / kKeys);
+                const int first = max(p.t0, p.kvt + (holed ? 0 : p.i0 / kKeys));
                 for (int t = first; ok && t < p.t1; ++t) {
                     const int base = (t - p.kvt) * kKeys;
-                    if (base + kKeys <= p.i0 + 1) continue;  // every row sees all of it
+                    const bool whole = base + kKeys <= p.i0 + 1;  // every row sees all of it
+                    if (whole && !holed) continue;
                     const uint32_t tile = tiles + (t - p.t0), vs = NK + tile % NV;
-                    if (!landed(1, tile)) break;
                     const int rows = min(kKeys, p.i1 - base);
+                    auto zero_holes = [&](uint32_t s) {
+                        for (int row = r_in; row < rows; row += kRowsStep)
+                            if (outside(__ldg(table + (p.kv + base + row) / a.P))) *cell(s, row, false) = make_uint4(0, 0, 0, 0);
+                        __syncwarp();
+                    };
+                    if (__builtin_expect(holed, 0)) {
+                        if (!landed(0, tile)) break;
+                        zero_holes(tile % NK);
+                        done(tile % NK);
+                        if (!landed(1, tile)) break;
+                        zero_holes(vs);
+                        if (whole) {
+                            done(vs);
+                            continue;
+                        }
+                    }
+                    if (!landed(1, tile)) break;
                     // a first pass over the rows looks for anything odd, eight loads at
                     // once; what it finds (hardly ever) is taken out one by one
                     uint32_t odd_any = 0;
@@ -979,6 +1025,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 ++n;
                 if (lane == 0) *(volatile uint32_t*)&sh->fixed = n;
             }
+            if (lane == 0) *(volatile uint32_t*)&sh->checked = n + 1;  // (the end of the pieces)
             while (more_new) more_new = append();
         }
     } else {

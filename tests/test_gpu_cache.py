@@ -318,6 +318,35 @@ def test_chunk_bad_page_reads_zeros(isd):
     c.upload().call().check(isd.FLAG_PAGE_OOB)
 
 
+BAD_PAGES = {
+    # name: Hq, Hkv, D, P, cached lengths, new tokens, (request, column) of the pages outside the pool
+    "in_the_last_cached_tile": (8, 2, 128, 4, [100, 33], [9, 1], [(0, 26), (1, 8)]),
+    "in_the_last_cached_tile_d64": (6, 2, 64, 8, [40, 3], [16, 2], [(0, 6), (1, 0)]),
+    "one_token": (4, 1, 128, 16, [128, 0, 64], [1, 1, 1], [(0, 8), (1, 0), (2, 4)]),
+    "tiles": (8, 2, 128, 16, [0, 200], [300, 70], [(0, 1), (0, 10), (1, 14)]),
+    "tiles_d64": (6, 2, 64, 24, [130, 0], [170, 400], [(0, 6), (0, 12), (1, 0), (1, 16)]),
+    "page_1": (4, 2, 64, 1, [5, 0], [200, 20], [(0, 3), (0, 5), (0, 100), (0, 204), (1, 19)]),
+    "page_3": (4, 1, 128, 3, [1], [300], [(0, 41), (0, 42), (0, 99)]),
+    "page_100": (4, 2, 128, 100, [150], [300], [(0, 2), (0, 4)]),
+    "page_256": (4, 1, 128, 256, [500], [140], [(0, 2)]),
+    "group_100": (100, 1, 64, 16, [140, 0], [30, 2], [(0, 9), (1, 0)]),
+    "long": (8, 4, 128, 16, [3000, 10], [700, 900], [(0, 200), (0, 231), (1, 30)]),
+}
+
+
+@pytest.mark.parametrize("name", BAD_PAGES)
+def test_chunk_new_tokens_on_bad_pages_are_zeros(isd, name):
+    """What a page outside the pool would hold counts as zeros for the tokens
+    that the call appends as it does for the cached ones, whatever they are."""
+    Hq, Hkv, D, P, ctx, n, bad = BAD_PAGES[name]
+    c = Chunk(isd, Hq, Hkv, D, P, ctx, n, seed=31)
+    for k, (b, col) in enumerate(bad):
+        c.table[b, col] = (-2, 10 ** 6, c.dims.num_pages)[k % 3]
+        for i in range(max(0, col * P - ctx[b]), min(n[b], (col + 1) * P - ctx[b])):
+            c.k_new[c.start[b] + i], c.v_new[c.start[b] + i] = float("nan"), float("nan")
+    c.upload().call().check(isd.FLAG_PAGE_OOB)
+
+
 @pytest.mark.parametrize("what", ["negative", "over"])
 def test_chunk_capacity(isd, what):
     c = Chunk(isd, 4, 2, 128, 16, [50, 60, 70], [20, 5, 30], seed=11).upload()
