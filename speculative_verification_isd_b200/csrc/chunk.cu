@@ -40,6 +40,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "chunk_cut.h"
 #include "common.cuh"
 #include "launch.h"
 #include "plan.h"
@@ -52,7 +53,6 @@ void set_error_detail(const char* msg);
 
 namespace {
 
-constexpr int kKeys = 128;              // keys per tile
 constexpr int kTileRows = 128;          // rows per tile
 constexpr int kHalfBytes = kKeys * 128; // 64 dimensions of a K, V or Q tile
 // A tile in shared memory is [64-d half][row][128 swizzled bytes].  A cached
@@ -61,15 +61,6 @@ constexpr int kHalfBytes = kKeys * 128; // 64 dimensions of a K, V or Q tile
 // (a TMA copy takes the producer about 70 cycles to issue).
 constexpr int kGroupRows = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr long long kMaxKeys = 1ll << 30;  // of a request: positions and tiles fit in 32 bits
-// New tokens that are put into the free rows of the last cached tile instead
-// of a tile of their own.
-constexpr int kMergeTokens = 16;
-// Cost of a key tile and of an item's start and end on the partition axis: an
-// item of two row tiles, and one of one.  Measured per CTA: 3.0 to 3.3 thousand
-// cycles for a tile of two and 9.5 thousand for its ends; 1.6 thousand and 7
-// thousand for one (2.5 thousand a tile when all CTAs wait for memory).
-constexpr int kCost2 = 4, kEnds2 = 13, kCost1 = 2, kEnds1 = 7;
 constexpr int kChunkThreads = 384;
 constexpr int kLaunchRegs = 168, kRegsLow = 88, kRegsHigh = 208;
 static_assert(kRegsLow * 128 + kRegsHigh * 256 <= kLaunchRegs * kChunkThreads, "register split exceeds the launch");
@@ -81,11 +72,10 @@ struct ChunkCut {
     int pad[3];
 };
 
-struct ChunkArgs {
-    int B, T, Hq, Hkv, grp, P, box, num_pages, max_pages;
-    int tpq, tps;   // tokens of a tile of 128 rows, and of one of 32
+struct ChunkArgs : CutShape {
+    int B, T, Hq, Hkv, grp, box, num_pages;
+    int tps;        // tokens of a tile of 32 rows
     int grouped;    // layout of a cached tile (see kGroup)
-    int two;        // whether T has items of two tiles
     int part_rows;  // rows of a partial result
     float scale_log2;
     const int32_t* page_table;
@@ -100,64 +90,6 @@ struct ChunkArgs {
     ChunkCut* cuts;  // [grid]
     int32_t* err_flag;
 };
-
-// New tokens of a request if its page list can hold them, else 0 (negative
-// or over-capacity length).  q_start is known to ascend within [0, T].
-ISD_DEVINL int chunk_tokens(const ChunkArgs& a, int kv, int n) {
-    if (kv < 0) return 0;
-    const long long t = (long long)kv + n;
-    return t > (long long)a.max_pages * a.P || t > kMaxKeys ? 0 : n;
-}
-
-// A request as the partition sees it.
-struct Request {
-    int n, kv, start;
-    int kvt;      // tiles with cached keys
-    bool merged;  // the new tokens lie in the last of them
-    int items;    // per KV head
-};
-
-ISD_DEVINL Request request_of(const ChunkArgs& a, int start, int end, int kv) {
-    Request r;
-    r.start = start;
-    r.kv = kv;
-    r.n = chunk_tokens(a, kv, end - start);
-    r.kvt = (max(kv, 0) + kKeys - 1) / kKeys;
-    r.merged = r.n <= kMergeTokens && r.n <= r.kvt * kKeys - kv;
-    r.items = (r.n + 2 * a.tpq - 1) / (2 * a.tpq);
-    return r;
-}
-
-struct Item {
-    int i0, i1;  // its tokens
-    bool two;
-    int nt, w, cost;  // key tiles, cost of one, of all
-};
-
-// Cost of a request's items of one KV head.
-ISD_DEVINL long long head_cost(const ChunkArgs& a, const Request& r) {
-    if (r.items == 0) return 0;
-    // all items but the last have two tiles; their new keys' tiles one by one
-    const int span = 2 * a.tpq, full = r.items - 1;
-    int fresh = 0;
-    if (!r.merged)
-        for (int q = 0, end = span; q < full; ++q, end += span) fresh += (end + kKeys - 1) / kKeys;
-    long long c = (long long)full * (kCost2 * (long long)r.kvt + kEnds2) + (long long)kCost2 * fresh;
-    const bool two = r.n - full * span > a.tpq;
-    const int nt = r.kvt + (r.merged ? 0 : (r.n + kKeys - 1) / kKeys);
-    return c + (two ? kCost2 * nt + kEnds2 : kCost1 * nt + kEnds1);
-}
-
-ISD_DEVINL Item item_of(const ChunkArgs& a, const Request& r, int q) {
-    Item it;
-    it.i0 = q * 2 * a.tpq;
-    it.i1 = min(r.n, it.i0 + 2 * a.tpq);
-    it.two = it.i1 - it.i0 > a.tpq;
-    it.nt = r.kvt + (r.merged ? 0 : (it.i1 + kKeys - 1) / kKeys);
-    it.w = it.two ? kCost2 : kCost1;
-    it.cost = it.w * it.nt + (it.two ? kEnds2 : kEnds1);
-    return it;
-}
 
 // This CTA's share of one item, as its roles see it.
 enum { kTwo = 0, kOne = 1, kQuad = 2 };
@@ -191,8 +123,8 @@ struct ChunkShared {
     uint64_t s_full[2], p_full[2][2], pv_half[2], pv_done[2], o_free[2];
     uint64_t meet, drain;
     Piece pieces[kPieces];
-    long long my0, total;
-    int len, rel, b, g, q;  // the range's length; its first item, which starts at `rel` in it
+    long long my0, total, len, rel;  // the range's start and length; its first item starts at `rel` in it
+    int b, g, q;
     Request first;
     uint32_t tmem;
     int abort_flag, never;
@@ -421,35 +353,23 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         };
         for (int b0 = 0; b0 < a.B; b0 += kChunkThreads) pass(b0 + (int)threadIdx.x);
         const long long total = run;
-        const long long most = a.two ? total / kCost2 : total / kCost1;  // every CTA between an item's ends has a tile of it
-        const int G = (int)min((long long)gridDim.x, max(most, 1ll));
+        const int G = cut_ctas(a, total, gridDim.x);
         const bool mine = (int)blockIdx.x < G;
-        long long my0 = 0, my1 = 0;
-        if (mine) {
-            if (total < (1 << 23)) {  // the products fit in 32 bits
-                my0 = (unsigned)total * blockIdx.x / (unsigned)G;
-                my1 = (unsigned)total * (blockIdx.x + 1) / (unsigned)G;
-            } else {
-                my0 = total * blockIdx.x / G;
-                my1 = total * (blockIdx.x + 1) / G;
-            }
-        }
+        const long long my0 = mine ? cut_start(total, G, blockIdx.x) : 0;
+        const long long my1 = mine ? cut_start(total, G, blockIdx.x + 1) : 0;
         if (threadIdx.x == 0) {
             sh->my0 = my0;
             sh->total = total;
-            sh->len = (int)(my1 - my0);
+            sh->len = my1 - my0;
         }
         auto locate = [&](int b) {
             if (my0 >= my1 || my0 < before || my0 >= before + head * a.Hkv) return;
-            long long rem = my0 - before;
-            int g = 0;
-            for (; rem >= head; ++g) rem -= head;
-            int q = 0;
-            for (int w; (w = item_of(a, r, q).cost) <= rem; ++q) rem -= w;
+            int g, q;
+            const int rem = cut_item(a, r, head, my0 - before, g, q);
             sh->b = b;
             sh->g = g;
             sh->q = q;
-            sh->rel = -(int)rem;
+            sh->rel = -rem;
             sh->first = r;
         };
         if (a.B <= kChunkThreads) {
@@ -710,17 +630,17 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 }
                 __syncwarp();
             };
-            int b = bad ? a.B : sh->b, g = sh->g, q = sh->q, rel = sh->rel;  // rel: the item's start less my0
-            const int len = sh->len;
+            int b = bad ? a.B : sh->b, g = sh->g, q = sh->q;
+            long long rel = sh->rel;  // the item's start less my0
+            const long long len = sh->len;
             Request r = sh->first;
             // the next piece of the walk; one without tiles at its end
             auto walk = [&](Piece& p) {
                 p.t0 = p.t1 = 0;
                 while (b < a.B && rel < len) {
                     const Item it = item_of(a, r, q);
-                    const int start = rel;
-                    if (start < 0) p.t0 = it.two ? (-start + kCost2 - 1) / kCost2 : (-start + kCost1 - 1) / kCost1;
-                    p.t1 = min(it.nt, it.two ? (len - start + kCost2 - 1) / kCost2 : (len - start + kCost1 - 1) / kCost1);
+                    const long long start = rel;
+                    cut_tiles(it, start, len, p.t0, p.t1);
                     p.b = b;
                     p.g = g;
                     p.start = r.start;
@@ -747,10 +667,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     if (p.t0 < p.t1) {
                         if (p.slot == 1 && lane == 0) {
                             // CTAs that hold a part: this one to the owner of the item's last tile
-                            const long long most = a.two ? sh->total / kCost2 : sh->total / kCost1;
-                            const int G = (int)min((long long)gridDim.x, max(most, 1ll));
-                            const long long last_at = sh->my0 + start + (long long)(it.nt - 1) * it.w;
-                            const int last = (int)(((last_at + 1) * G - 1) / sh->total);
+                            const int G = cut_ctas(a, sh->total, gridDim.x);
+                            const int last =
+                                cut_owner(sh->total, G, sh->my0 + start + (long long)(it.nt - 1) * it.w);
                             ChunkCut c = {last - (int)blockIdx.x + 1, p.g, it.i0, it.i1, p.start, {0, 0, 0}};
                             a.cuts[blockIdx.x] = c;
                         }
