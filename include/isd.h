@@ -537,11 +537,10 @@ isd_status isd_layers(const isd_dims* d, int32_t n_layers, int32_t inter, float 
  * (any positive values).  Workspace: isd_chunk_workspace_bytes(d, T) bytes,
  * 256-aligned (0 for invalid dims or T < 0); one made for a larger T serves.
  * Errors: a null pointer, invalid dims, T < 0, an sm_scale that is not
- * positive and finite, a tensor that is not 16-byte aligned, an out
- * that overlaps an input, or a pool that overlaps the other one, q, k_new or
- * v_new -> ISD_ERR_INVALID_ARG; a shape not supported ->
- * ISD_ERR_UNSUPPORTED_SHAPE; a workspace too small or misaligned ->
- * ISD_ERR_WORKSPACE.  On the device: ISD_FLAG_CHUNK_RANGE (no request is
+ * positive and finite, a tensor that is not 16-byte aligned, or an out, a
+ * pool, a workspace or an err_flag that overlaps another buffer of the call ->
+ * ISD_ERR_INVALID_ARG; a shape not supported -> ISD_ERR_UNSUPPORTED_SHAPE; a
+ * workspace too small or misaligned -> ISD_ERR_WORKSPACE.  On the device: ISD_FLAG_CHUNK_RANGE (no request is
  * served); ISD_FLAG_CAPACITY (a request with a negative kv_len or tokens past
  * its pages or 2^30: its rows of out are zero, its cache is left alone);
  * ISD_FLAG_PAGE_OOB (keys and values on a page id outside the pool, cached or

@@ -713,6 +713,25 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// A buffer of a call; an absent one is empty.
+struct Span {
+    const void* p;
+    size_t n;
+};
+
+// Whether a buffer that the call writes overlaps another of its buffers.
+template <int W, int R>
+bool any_overlap(const Span (&written)[W], const Span (&read)[R]) {
+    for (int i = 0; i < W; ++i) {
+        if (!written[i].n) continue;
+        for (int j = 0; j < i; ++j)
+            if (written[j].n && overlaps(written[i].p, written[i].n, written[j].p, written[j].n)) return true;
+        for (int j = 0; j < R; ++j)
+            if (read[j].n && overlaps(written[i].p, written[i].n, read[j].p, read[j].n)) return true;
+    }
+    return false;
+}
+
 isd_status check_ws_bytes(size_t need, void* ws, size_t ws_bytes) {
     if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255)) {
         snprintf(g_last_error, sizeof(g_last_error), "workspace: need %zu bytes, 256-aligned", need);
@@ -758,14 +777,12 @@ isd_status isd_chunk_attention(const isd_dims* d, int32_t T, const uint16_t* q,
     if (T == 0) return ISD_OK;
     const size_t out_n = (size_t)T * d->Hq * d->D * 2, new_n = (size_t)T * d->Hkv * d->D * 2;
     const size_t pool_n = (size_t)d->num_pages * d->page_size * d->Hkv * d->D * 2;
-    if (overlaps(out, out_n, q, out_n) || overlaps(out, out_n, k_new, new_n) || overlaps(out, out_n, v_new, new_n) ||
-        overlaps(out, out_n, k_pool, pool_n) || overlaps(out, out_n, v_pool, pool_n))
-        return invalid("out overlaps an input");
-    if (overlaps(k_pool, pool_n, v_pool, pool_n) || overlaps(k_new, new_n, k_pool, pool_n) ||
-        overlaps(k_new, new_n, v_pool, pool_n) || overlaps(v_new, new_n, k_pool, pool_n) ||
-        overlaps(v_new, new_n, v_pool, pool_n) || overlaps(q, out_n, k_pool, pool_n) ||
-        overlaps(q, out_n, v_pool, pool_n))
-        return invalid("a pool overlaps the other one or an input");
+    const size_t b4 = (size_t)d->B * 4;
+    const Span written[] = {{out, out_n}, {k_pool, pool_n}, {v_pool, pool_n}, {ws, isd::chunk_ws_bytes(d, T)},
+                            {err_flag, err_flag ? (size_t)4 : 0}};
+    const Span read[] = {{q, out_n}, {k_new, new_n}, {v_new, new_n}, {page_table, b4 * d->max_pages_per_req},
+                         {kv_len, b4}, {q_start, b4 + 4}};
+    if (any_overlap(written, read)) return invalid("out, a pool, the workspace or the flag overlaps another buffer");
     ISD_CUDA(isd::launch_chunk_attention(d, T, q, k_new, v_new, k_pool, v_pool, page_table, kv_len,
                                          q_start, out, ws, err_flag, static_cast<cudaStream_t>(stream)));
     return ISD_OK;

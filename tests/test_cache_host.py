@@ -125,6 +125,35 @@ def test_chunk_refusals(isd):
     assert call(T=0) == isd.ISD_OK
 
 
+def test_chunk_refuses_overlaps(isd):
+    """What the call writes (out, the pools, the workspace, the flag) overlaps
+    nothing else, from the first byte to the last."""
+    lib = isd.library()
+    d, T = _dims(isd), 100
+    need = isd.chunk_workspace_bytes(d, T)
+    pool = d.num_pages * d.page_size * d.Hkv * d.D * 2
+    # q, k_new, v_new, k_pool, v_pool, page_table, kv_len, q_start, out, ws, err_flag
+    size = [T * 4 * 128 * 2, T * 2 * 128 * 2, T * 2 * 128 * 2, pool, pool, 2 * 4 * 4, 2 * 4, 3 * 4, T * 4 * 128 * 2, need, 4]
+    align = [16] * 5 + [4] * 3 + [16, 256, 4]
+    written = {3, 4, 8, 9, 10}
+
+    def call(p, T=T):
+        return lib.isd_chunk_attention(ctypes.byref(d), T, *map(ctypes.c_void_p, p[:9]), ctypes.c_void_p(p[9]), need,
+                                       ctypes.c_void_p(p[10]), None)
+
+    for i in range(11):
+        for j in range(11):
+            if i == j or not {i, j} & written:
+                continue
+            p = [(1 + k) << 28 for k in range(11)]
+            # the last bytes of j under the first of i, as far as i's alignment goes
+            p[i] = (p[j] + size[j] - 1) // align[i] * align[i]
+            assert call(p) == isd.ISD_ERR_INVALID_ARG, (i, j)
+            p[i] = p[j]
+            if p[j] % align[i] == 0:
+                assert call(p) == isd.ISD_ERR_INVALID_ARG, (i, j)
+
+
 def test_fork_refusals(isd):
     lib = isd.library()
     at = lambda k: ctypes.c_void_p((1 + k) << 20)  # noqa: E731
