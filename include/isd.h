@@ -564,9 +564,9 @@ isd_status isd_chunk_attention(const isd_dims* d, int32_t T, const uint16_t* q,
  *   next_free_page [1] int32: this batch's state (isd_prepare_block's)
  *   pools  HOST array of n_pools device pointers, each [num_pages, page_size,
  *          Hkv, D] bf16: every layer's k_pool and v_pool
- * Outputs (int32; none may overlap an input): next_kv_len, next_pages_used
- * [R], next_page_table [R, max_pages_per_req] (-1 past pages_used),
- * next_free_out [1].
+ * Outputs (int32; none may overlap an input, a pool, or another output):
+ * next_kv_len, next_pages_used [R], next_page_table [R, max_pages_per_req] (-1
+ * past pages_used), next_free_out [1].
  *  - The first slot that names a request keeps its page list; each further one
  *    shares the pages that are full (kv_len / P of them; no later step writes
  *    there) and gets its own copy of the rows of the part-filled page.
@@ -578,7 +578,9 @@ isd_status isd_chunk_attention(const isd_dims* d, int32_t T, const uint16_t* q,
  * Supported: Hkv * D * 2 bytes (a token) a multiple of 16; B + R <= 12000.
  * N, V, Hq and sm_scale are not used.
  * Errors: invalid dims, R < 1, n_pools < 0, a null or misaligned pointer, an
- * output that is also an input -> ISD_ERR_INVALID_ARG; else
+ * output or err_flag that overlaps another buffer, a pool that overlaps a
+ * buffer or lies across another pool (it may be listed twice) ->
+ * ISD_ERR_INVALID_ARG; else
  * ISD_ERR_UNSUPPORTED_SHAPE.  On the device a slot that cannot be made is left
  * empty (length 0, no pages): ISD_FLAG_PARENT_OOB, or ISD_FLAG_CAPACITY (page
  * list longer than the table or than the pool has left, in slot order; a

@@ -748,6 +748,37 @@ isd_status check_pools(const isd_dims* d, int32_t n_pools, uint16_t* const* pool
     return ISD_OK;
 }
 
+// Whether a pool lies across another one (the same one twice is copied to the
+// same bytes twice) or on one of the call's other buffers.
+template <int W, int R>
+bool pools_overlap(const isd_dims* d, int32_t n_pools, uint16_t* const* pools, const Span (&written)[W],
+                   const Span (&read)[R]) {
+    const size_t bytes = (size_t)d->num_pages * d->page_size * d->Hkv * d->D * 2;
+    const auto at = [&](int32_t i) { return reinterpret_cast<uintptr_t>(pools[i]); };
+    uintptr_t low = UINTPTR_MAX, high = 0;
+    bool ascending = true;  // (as a rule they do, one allocated after the other)
+    for (int32_t i = 0; i < n_pools; ++i) {
+        if (i && at(i) < high) ascending = false;
+        if (at(i) < low) low = at(i);
+        if (at(i) + bytes > high) high = at(i) + bytes;
+    }
+    const auto on_a_pool = [&](const Span& s) {
+        if (!s.n || reinterpret_cast<uintptr_t>(s.p) >= high || low >= reinterpret_cast<uintptr_t>(s.p) + s.n) return false;
+        for (int32_t i = 0; i < n_pools; ++i)
+            if (overlaps(s.p, s.n, pools[i], bytes)) return true;
+        return false;
+    };
+    for (const Span& s : written)
+        if (on_a_pool(s)) return true;
+    for (const Span& s : read)
+        if (on_a_pool(s)) return true;
+    if (ascending) return false;
+    for (int32_t i = 0; i < n_pools; ++i)
+        for (int32_t j = 0; j < i; ++j)
+            if (at(i) != at(j) && at(i) < at(j) + bytes && at(j) < at(i) + bytes) return true;
+    return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -803,14 +834,12 @@ isd_status isd_fork_requests(const isd_dims* d, int32_t R, const int32_t* parent
     ISD_TRY(check_pools(d, n_pools, pools));
     if ((int64_t)d->B + R > 12000) return unsupported("B + R must be <= 12000");
     const size_t cols = (size_t)d->max_pages_per_req * 4, b4 = (size_t)d->B * 4, r4 = (size_t)R * 4;
-    const void* in[6] = {parent, reserve, kv_len, pages_used, page_table, next_free_page};
-    const size_t in_n[6] = {r4, reserve ? r4 : 0, b4, b4, d->B * cols, 4};
-    const void* outs[4] = {next_kv_len, next_pages_used, next_page_table, next_free_out};
-    const size_t out_n[4] = {r4, r4, R * cols, 4};
-    for (int o = 0; o < 4; ++o)
-        for (int i = 0; i < 6; ++i)
-            if (in_n[i] && overlaps(outs[o], out_n[o], in[i], in_n[i]))
-                return invalid("a fork output overlaps an input");
+    const Span read[] = {{parent, r4}, {reserve, reserve ? r4 : 0}, {kv_len, b4}, {pages_used, b4},
+                         {page_table, d->B * cols}, {next_free_page, 4}};
+    const Span written[] = {{next_kv_len, r4}, {next_pages_used, r4}, {next_page_table, R * cols}, {next_free_out, 4},
+                            {err_flag, err_flag ? (size_t)4 : 0}};
+    if (any_overlap(written, read)) return invalid("a fork output overlaps another buffer");
+    if (pools_overlap(d, n_pools, pools, written, read)) return invalid("a pool overlaps another one or a buffer");
     ISD_CUDA(isd::launch_fork(d, R, parent, reserve, kv_len, pages_used, page_table, next_free_page,
                               n_pools, pools, next_kv_len, next_pages_used, next_page_table,
                               next_free_out, err_flag, static_cast<cudaStream_t>(stream)));

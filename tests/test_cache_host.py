@@ -188,6 +188,39 @@ def test_fork_refusals(isd):
     assert call(dd=bad) == isd.ISD_ERR_INVALID_ARG
 
 
+def test_fork_refuses_overlaps(isd):
+    """Outputs and the flag lie apart from each other and from the inputs, the
+    pools from all of them and from each other, to the last byte."""
+    lib = isd.library()
+    d, R = _dims(isd), 3
+    pool = d.num_pages * d.page_size * d.Hkv * d.D * 2
+    table = 4 * d.max_pages_per_req
+    # parent, reserve, kv_len, pages_used, page_table, next_free_page, the four outputs, err_flag
+    size = [12, 12, 8, 8, 2 * table, 4, 12, 12, 3 * table, 4, 4]
+
+    def call(p, pools):
+        return lib.isd_fork_requests(ctypes.byref(d), R, *map(ctypes.c_void_p, p[:6]), len(pools),
+                                     (ctypes.c_void_p * len(pools))(*pools), *map(ctypes.c_void_p, p[6:]), None)
+
+    apart = [1 << 40, 1 << 41, 1 << 42]
+    for i in range(11):
+        for j in range(6, 11):
+            if i == j:
+                continue
+            p = [(1 + k) << 20 for k in range(11)]
+            for at in (p[j], p[j] + size[j] - 4, p[j] - size[i] + 4):
+                p[i] = at
+                assert call(p, apart) == isd.ISD_ERR_INVALID_ARG, (i, j)
+    for i in range(11):   # a pool's first and last bytes
+        for at in (apart[1] - size[i] + 4, apart[1] + pool - 4):
+            p = [(1 + k) << 20 for k in range(11)]
+            p[i] = at
+            assert call(p, apart) == isd.ISD_ERR_INVALID_ARG, i
+    p = [(1 + k) << 20 for k in range(11)]
+    for pools in ([1 << 40, (1 << 40) + pool - 16], [(1 << 40) + 16, 1 << 41, 1 << 40], [1 << 41, 1 << 40, (1 << 41) - 16]):
+        assert call(p, pools) == isd.ISD_ERR_INVALID_ARG
+
+
 def test_compact_refusals(isd):
     lib = isd.library()
     fake = ctypes.c_void_p(1 << 20)
