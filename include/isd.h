@@ -604,7 +604,7 @@ isd_status isd_fork_requests(const isd_dims* d, int32_t R, const int32_t* parent
  *   (every pool moves the same pages)
  *   next_page_table [B, max_pages_per_req] int32 (may be page_table itself):
  *          the table after the move, -1 past pages_used; next_free_out [1] = L
- * (Otherwise the outputs overlap no input and not each other.)
+ * (Otherwise the outputs, the workspace and err_flag overlap no other buffer.)
  * A page that several requests share moves once.  Pages from L on keep their
  * bytes, so the call can be repeated on the same inputs.
  * Workspace: isd_pages_workspace_bytes(d) bytes, 256-aligned.  Supported as

@@ -858,12 +858,13 @@ isd_status isd_compact_pages(const isd_dims* d, const int32_t* pages_used,
     ISD_TRY(check_ws_bytes(isd::pages_ws_bytes(d), ws, ws_bytes));
     if (!pages_used || !page_table || !next_page_table || !next_free_out)
         return invalid("null compact pointer");
-    const size_t table_n = (size_t)d->B * d->max_pages_per_req * 4, used_n = (size_t)d->B * 4;
-    if ((next_page_table != page_table && overlaps(next_page_table, table_n, page_table, table_n)) ||
-        overlaps(next_page_table, table_n, pages_used, used_n) || overlaps(next_free_out, 4, pages_used, used_n) ||
-        overlaps(next_free_out, 4, page_table, table_n) || overlaps(next_free_out, 4, next_page_table, table_n))
-        return invalid("a compact output overlaps an input or the other one");
     ISD_TRY(check_pools(d, n_pools, pools));
+    const size_t table_n = (size_t)d->B * d->max_pages_per_req * 4;
+    const Span read[] = {{pages_used, (size_t)d->B * 4}, {page_table, next_page_table != page_table ? table_n : 0}};
+    const Span written[] = {{next_page_table, table_n}, {next_free_out, 4}, {ws, isd::pages_ws_bytes(d)},
+                            {err_flag, err_flag ? (size_t)4 : 0}};
+    if (any_overlap(written, read)) return invalid("a compact output, the workspace or the flag overlaps another buffer");
+    if (pools_overlap(d, n_pools, pools, written, read)) return invalid("a pool overlaps another one or a buffer");
     ISD_CUDA(isd::launch_compact(d, pages_used, page_table, n_pools, pools, next_page_table,
                                  next_free_out, ws, err_flag, static_cast<cudaStream_t>(stream)));
     return ISD_OK;

@@ -255,6 +255,40 @@ def test_compact_refusals(isd):
     assert isd.pages_workspace_bytes(bad) == 0
 
 
+def test_compact_refuses_overlaps(isd):
+    lib = isd.library()
+    d = _dims(isd)
+    need = isd.pages_workspace_bytes(d)
+    pool = d.num_pages * d.page_size * d.Hkv * d.D * 2
+    table = 4 * d.B * d.max_pages_per_req
+    # pages_used, page_table, next_page_table, next_free_out, ws, err_flag
+    size, align = [8, table, table, 4, need, 4], [4, 4, 4, 4, 256, 4]
+
+    def call(p, pools):
+        return lib.isd_compact_pages(ctypes.byref(d), *map(ctypes.c_void_p, p[:2]), len(pools),
+                                     (ctypes.c_void_p * len(pools))(*pools), *map(ctypes.c_void_p, p[2:5]), need,
+                                     ctypes.c_void_p(p[5]), None)
+
+    apart = [1 << 40, 1 << 41, 1 << 42]
+    for i in range(6):
+        for j in range(2, 6):
+            if i == j:
+                continue
+            p = [(1 + k) << 20 for k in range(6)]
+            for at in (p[j], (p[j] + size[j] - 1) // align[i] * align[i]):
+                if (i, j, at) == (1, 2, p[2]):
+                    continue   # the new table in the old one's place
+                p[i] = at
+                assert call(p, apart) == isd.ISD_ERR_INVALID_ARG, (i, j)
+    for i in range(6):
+        p = [(1 + k) << 20 for k in range(6)]
+        p[i] = (apart[1] + pool - 1) // align[i] * align[i]
+        assert call(p, apart) == isd.ISD_ERR_INVALID_ARG, i
+    p = [(1 + k) << 20 for k in range(6)]
+    for pools in ([1 << 40, (1 << 40) + pool - 16], [(1 << 40) + 16, 1 << 41, 1 << 40]):
+        assert call(p, pools) == isd.ISD_ERR_INVALID_ARG
+
+
 def test_binding_refuses_host_tensors(isd):
     import torch
     d = _dims(isd)
