@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kPageThreads) mark_kernel(const __grid_constan
 // place before L.  One CTA writes the list of moves.
 template <int THREADS>
 ISD_DEVINL int list_moves(const CompactArgs& a, const uint32_t* live, int* part) {
-    const int words = (a.num_pages + 31) / 32;
+    const int words = (a.num_pages - 1) / 32 + 1;
     int count = 0;
     for (int w0 = 0; w0 < words; w0 += THREADS) {
         const int w = w0 + (int)threadIdx.x;
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kSmallThreads) plan_small_kernel(const __grid_
     extern __shared__ uint32_t live[];
     __shared__ int part[kSmallThreads / 32];
     pdl_trigger();
-    const int words = (a.num_pages + 31) / 32, cells = a.B * a.max_pages;
+    const int words = (a.num_pages - 1) / 32 + 1, cells = a.B * a.max_pages;
     for (int w = threadIdx.x; w < words; w += kSmallThreads) live[w] = 0;
     for (int b = threadIdx.x; b < a.B; b += kSmallThreads) {
         const int used = a.pages_used[b];
@@ -397,10 +397,10 @@ cudaError_t launch_compact(const isd_dims* d, const int32_t* pages_used, const i
     a.page_table = page_table;
     a.next_table = next_table;
     a.next_free_out = next_free_out;
+    const size_t bitmap = page_bitmap_bytes(d->num_pages);
     a.live = static_cast<uint32_t*>(ws);
-    a.moves = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + align_up((size_t)(d->num_pages + 31) / 32 * 4, 256));
+    a.moves = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + align_up(bitmap, 256));
     a.err_flag = err_flag;
-    const size_t bitmap = (size_t)(d->num_pages + 31) / 32 * 4;
     const bool small = d->num_pages <= kSmallPages && (long long)d->B * d->max_pages_per_req <= kSmallCells;
     cudaError_t e;
     if (small) {

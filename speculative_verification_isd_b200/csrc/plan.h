@@ -78,8 +78,9 @@ struct PoolList {
 
 // Workspace of isd_compact_pages: a bitmap of the pages in use, then the
 // number of moves, their old and new places, and the new place by old page.
+inline size_t page_bitmap_bytes(int32_t num_pages) { return ((size_t)num_pages + 31) / 32 * 4; }
 inline size_t pages_ws_bytes(const isd_dims* d) {
-    return align_up((size_t)(d->num_pages + 31) / 32 * 4, 256) +
+    return align_up(page_bitmap_bytes(d->num_pages), 256) +
            align_up((1 + 3 * (size_t)d->num_pages) * 4, 256);
 }
 

@@ -255,6 +255,14 @@ def test_compact_refusals(isd):
     assert isd.pages_workspace_bytes(bad) == 0
 
 
+@pytest.mark.parametrize("pages", [1, 32, 33, 2 ** 31 - 32, 2 ** 31 - 31, 2 ** 31 - 1])
+def test_compact_workspace_of_many_pages(isd, pages):
+    """A bit per page in 4-byte words, and three numbers per page and one, each
+    part rounded up to 256 bytes."""
+    up = lambda n: -(-n // 256) * 256  # noqa: E731
+    assert isd.pages_workspace_bytes(_dims(isd, num_pages=pages)) == up(-(-pages // 32) * 4) + up((1 + 3 * pages) * 4)
+
+
 def test_compact_refuses_overlaps(isd):
     lib = isd.library()
     d = _dims(isd)
