@@ -475,7 +475,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 auto wait = [&](uint64_t* bar, uint32_t par) {
                     const bool good = mbar_wait_bounded(bar, par & 1, abort_flag, kWaitNs);
                     if (!good) give_up();
-                    ok = __all_sync(0xffffffffu, good);
+                    ok = __all_sync(0xffffffffu, good) && ok;  // (a later wait may find its phase done)
                     return ok;
                 };
                 auto wait_q = [&](int s) {
