@@ -393,13 +393,21 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         *abort_flag = 1;
         raise_flag(a.err_flag, ISD_FLAG_WAIT_TIMEOUT);
     };
-    // waits on a counter in shared memory; every lane that asks gets the answer
+    // waits on a counter in shared memory; every lane that asks gets the answer.  The
+    // limit runs from the counter's last step: the fixing warp waits for the last
+    // tile of a piece from its first on, whose millions of tiles may take seconds.
     auto until = [&](const uint32_t* counter, uint32_t least) {
-        if (peek(counter) >= least) return true;
-        const uint64_t t_start = global_ns();
+        uint32_t at = peek(counter);
+        if (at >= least) return true;
+        uint64_t t_step = global_ns();
         for (uint32_t it = 1; peek(counter) < least; ++it) {
             __nanosleep(20);
-            if ((it & 63) == 0 && (*abort_flag || global_ns() - t_start > kWaitNs)) {
+            if (it & 63) continue;
+            if (const uint32_t now = peek(counter); now != at) {
+                at = now;
+                t_step = global_ns();
+            }
+            if (*abort_flag || global_ns() - t_step > kWaitNs) {
                 give_up();
                 return false;
             }

@@ -181,6 +181,26 @@ def test_chunk_one_long_request_many_parts(isd):
     Chunk(isd, 4, 1, 64, 16, [18000], [20], seed=7).upload().call().check()
 
 
+def test_chunk_piece_of_seconds(isd):
+    """A piece of 2^22 tiles per CTA (2.6 s): no wait gives up while the others go
+    on.  The requests' pages are one and the same; scores 0 and values 1 make every
+    sum a whole number that 32 bits hold, and the result 1."""
+    kv, P, D = (1 << 29) + 5, 1024, 64
+    B = torch.cuda.get_device_properties(0).multi_processor_count
+    cols = kv // P + 1
+    table = torch.zeros(B, cols, dtype=torch.int32, device="cuda")
+    table[:, -1] = torch.arange(1, B + 1, dtype=torch.int32, device="cuda")   # the new tokens' own pages
+    zeros, ones = (torch.full((B + 1, P, 1, D), x, dtype=torch.bfloat16, device="cuda") for x in (0.0, 1.0))
+    q = bf16(np.random.default_rng(1), B, 1, D).cuda()
+    d = isd.make_dims(B, 1, 1, 1, D, 1, P, B + 1, cols)
+    out, err = torch.zeros(B, D, dtype=torch.bfloat16, device="cuda"), i32([0])
+    isd.chunk_attention(d, q, torch.zeros_like(q), torch.ones_like(q), zeros, ones, table, i32([kv] * B),
+                        i32(np.arange(B + 1)), out, isd.alloc_chunk_workspace(d, B), err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert (out == 1).all()
+
+
 @pytest.mark.parametrize("gain", [1.0, 20.0])
 @pytest.mark.parametrize("name", LONG)
 def test_chunk_long_pieces(isd, name, gain):
