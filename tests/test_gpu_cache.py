@@ -447,6 +447,20 @@ def test_chunk_no_rows(isd):
         assert torch.equal(p.view(torch.int16), k.view(torch.int16))
 
 
+@pytest.mark.parametrize("before,after", [(9, 0), (0, 300), (130, 70)])
+def test_chunk_rows_of_no_request_only(isd, before, after):
+    """Rows, none of them a request's: the kernel runs and writes nothing."""
+    c = Chunk(isd, 8, 2, 128, 16, [10, 300, 0], [0, 0, 0], seed=17, before=before, after=after).upload()
+    keep = [p.clone() for p in c.d_pool]
+    for _ in range(2):
+        c.call()
+    torch.cuda.synchronize()
+    assert int(c.err.item()) == 0
+    assert (c.out == 7).all()
+    for p, k in zip(c.d_pool, keep):
+        assert torch.equal(p.view(torch.int16), k.view(torch.int16))
+
+
 @pytest.mark.parametrize("P", [16, 20])
 def test_far_pages(isd, P):
     """Pages past 2^32 bytes and 2^31 elements of a pool: the same results as in
@@ -588,6 +602,15 @@ def test_fork_faults(isd):
     c.err.zero_()
     c.used[2] = 3
     check_fork(isd, c, [2, 1], flags=isd.FLAG_CAPACITY)
+
+
+def test_pool_listed_twice(isd):
+    """It is copied, and moved, to the same bytes twice."""
+    c = Cache(isd, 3, 16, [33, 16, 100], spare=60, extra=[1, 0, 2], cols=20, seed=5)
+    c.pools = [c.pools[1], c.pools[0], c.pools[1]]
+    check_fork(isd, c, [0, 2, 2, 0])
+    c.used[0] = 0
+    check_compact(isd, c)
 
 
 def test_fork_bad_page(isd):
