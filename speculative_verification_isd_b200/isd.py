@@ -604,12 +604,13 @@ class ChunkCall:
     constructor takes the arguments of ``chunk_attention`` and validates them;
     calling the object passes the cached pointers to the library.  With
     stream=None each call goes to the stream that is current then.  The tensors
-    must stay alive and in place while the object is used."""
+    must stay alive and in place while the object is used; the dims are copied."""
 
     def __init__(self, d: Dims, q, k_new, v_new, k_pool, v_pool, page_table, kv_len, q_start, out,
                  ws, err_flag=None, stream=None):
         if d.Hq < 1 or d.Hkv < 1 or d.D < 1:
             raise IsdError(ISD_ERR_INVALID_ARG)
+        d = Dims.from_buffer_copy(d)  # the tensors are checked against these, not against what d becomes
         T = q.numel() // (d.Hq * d.D)
         kvrow, bf16 = d.page_size * d.Hkv * d.D, torch.bfloat16
         named = [

@@ -313,6 +313,26 @@ def test_binding_refuses_host_tensors(isd):
         isd.fork_requests(_dims(isd, num_pages=11), z, z, z, z, z, isd.pool_array(d, []), z, z, z, z)
 
 
+def test_chunk_call_keeps_the_dims_it_checked(isd, monkeypatch):
+    """Dims changed after the check do not reach the kernel with tensors that
+    were never compared with them."""
+    import torch
+    seen = {}
+
+    def pointers(named):
+        seen.update((name, n) for name, _, _, n in named)
+        return [None] * len(named), 0
+
+    monkeypatch.setattr(isd, "_pointers", pointers)
+    d = _dims(isd)
+    t = torch.zeros(3 * 4 * 128, dtype=torch.bfloat16)
+    call = isd.ChunkCall(d, *[t] * 10, torch.zeros(8, dtype=torch.uint8))
+    d.B, d.max_pages_per_req, d.num_pages = 64, 1 << 20, 1 << 20
+    kept = call._args[0]._obj
+    assert (kept.B, kept.max_pages_per_req, kept.num_pages) == (2, 4, 10)
+    assert seen["page_table"] == 8 and seen["q_start"] == 3
+
+
 def test_rounding_constants():
     """The half steps the GPU tests' tolerances count with."""
     import torch
