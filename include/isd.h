@@ -59,7 +59,7 @@ typedef int32_t isd_status;
 #define ISD_FLAG_TOKEN_OOB     2  /* a clean token outside [0, V) */
 #define ISD_FLAG_NCLEAN_RANGE  4  /* n_clean outside [1, N] */
 #define ISD_FLAG_CAPACITY      8  /* kv_len + block exceeds the request's page capacity */
-#define ISD_FLAG_WAIT_TIMEOUT 16  /* a bounded on-chip wait gave up (LM-head pipeline) */
+#define ISD_FLAG_WAIT_TIMEOUT 16  /* a bounded on-chip wait gave up (attention, LM head, accept) */
 #define ISD_FLAG_CHUNK_RANGE  32  /* q_start does not ascend within [0, T] */
 #define ISD_FLAG_PARENT_OOB   64  /* a parent outside [-1, B) */
 
@@ -540,12 +540,17 @@ isd_status isd_layers(const isd_dims* d, int32_t n_layers, int32_t inter, float 
  * positive and finite, a tensor that is not 16-byte aligned, or an out, a
  * pool, a workspace or an err_flag that overlaps another buffer of the call ->
  * ISD_ERR_INVALID_ARG; a shape not supported -> ISD_ERR_UNSUPPORTED_SHAPE; a
- * workspace too small or misaligned -> ISD_ERR_WORKSPACE.  On the device: ISD_FLAG_CHUNK_RANGE (no request is
- * served); ISD_FLAG_CAPACITY (a request with a negative kv_len or tokens past
- * its pages or 2^30: its rows of out are zero, its cache is left alone);
- * ISD_FLAG_PAGE_OOB (keys and values on a page id outside the pool, cached or
- * new, read as zeros, and are not written).  Two calls may overlap on the GPU if their
- * workspaces and the cache rows they write differ.
+ * workspace too small or misaligned -> ISD_ERR_WORKSPACE.  On the device:
+ *  - ISD_FLAG_CHUNK_RANGE: no request is served;
+ *  - ISD_FLAG_CAPACITY: a request with a negative kv_len, or tokens past its
+ *    pages or 2^30: its rows of out are zero, its cache is left alone;
+ *  - ISD_FLAG_PAGE_OOB: keys and values on a page id outside the pool, cached
+ *    or new, read as zeros, and are not written;
+ *  - ISD_FLAG_WAIT_TIMEOUT (an internal wait saw no progress for 2 s): any row
+ *    of out may be wrong or missing; the new K/V rows are written all the same,
+ *    and the call can be repeated.
+ * Two calls may overlap on the GPU if their workspaces and the cache rows they
+ * write differ.
  */
 size_t isd_chunk_workspace_bytes(const isd_dims* d, int32_t T);
 isd_status isd_chunk_attention(const isd_dims* d, int32_t T, const uint16_t* q,
@@ -572,6 +577,11 @@ isd_status isd_chunk_attention(const isd_dims* d, int32_t T, const uint16_t* q,
  *    there) and gets its own copy of the rows of the part-filled page.
  *  - Page lists are then extended to ceil((kv_len + reserve) / P) pages.  New
  *    pages come in slot order from *next_free_page on.
+ *  - What else a request has by slot is the caller's to gather by the same
+ *    parents: of an ISD batch n_clean, clean_tok, and the last step's logits and
+ *    row_stats (its Q rows of each; a step reads them where n_clean > 1).  An
+ *    empty slot is a request of length 0 without pages: the steps serve it like
+ *    any other, so it takes a new request's n_clean and clean_tok.
  *  - Of the pools, only pages from *next_free_page on are written.  Nothing of
  *    the old batch's state changes: the call can be repeated, or the new state
  *    be thrown away.
