@@ -877,22 +877,31 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     const int fresh = p.merged ? p.i1 : 0;
                     uint32_t zeros = 0;  // bit i: token i lies on a page outside the pool
                     auto new_chunk = [&](const __nv_bfloat16* src, int i) {
-                        if (zeros >> i & 1) return make_uint4(0, 0, 0, 0);
                         return __ldg(reinterpret_cast<const uint4*>(src + ((size_t)(p.start + i) * a.Hkv + p.g) * D) + ch);
                     };
+                    uint4 k_next = make_uint4(0, 0, 0, 0), v_next = k_next;  // fetched while the tile is on its way
                     if (fresh) {
                         int id = 0;
                         if (lane < fresh) id = __ldg(table + (p.kv + lane) / a.P);
+                        if (r_in < fresh) {
+                            k_next = new_chunk(a.k_new, r_in);
+                            v_next = new_chunk(a.v_new, r_in);
+                        }
                         if (!landed(0, tile)) break;
                         zeros = __ballot_sync(0xffffffffu, outside(id));
-                        for (int i = r_in; i < fresh; i += kRowsStep) *cell(ks, m + i, a.grouped) = new_chunk(a.k_new, i);
+                        for (int i = r_in; i < fresh; i += kRowsStep) {
+                            *cell(ks, m + i, a.grouped) = zeros >> i & 1 ? make_uint4(0, 0, 0, 0) : k_next;
+                            if (i + kRowsStep < fresh) k_next = new_chunk(a.k_new, i + kRowsStep);
+                        }
                         done(ks);
                     }
                     if (!landed(1, tile)) break;
                     for (int i0 = 0; i0 < fresh; i0 += kRowsStep) {
                         const int i = i0 + r_in;
-                        uint4 w = make_uint4(0, 0, 0, 0);
-                        if (i < fresh) w = new_chunk(a.v_new, i);
+                        uint4 w = v_next;
+                        if (i < fresh && (zeros >> i & 1)) w = make_uint4(0, 0, 0, 0);
+                        if (i + kRowsStep < fresh) v_next = new_chunk(a.v_new, i + kRowsStep);
+                        else v_next = make_uint4(0, 0, 0, 0);
                         const bool odd = odd_bits(w) & kOddBits;
                         if (__any_sync(0xffffffffu, odd)) {
                             if (!claim()) break;

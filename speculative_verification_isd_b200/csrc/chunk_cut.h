@@ -114,9 +114,10 @@ ISD_CUT int cut_item(const CutShape& a, const Request& r, long long head, long l
 // The tiles [t0, t1) of an item that starts at `start` in a range of length
 // `len` (none: only a part of its ends lies there).
 ISD_CUT void cut_tiles(const Item& it, long long start, long long len, int& t0, int& t1) {
-    const int w = it.w;
-    t0 = start < 0 ? ((int)-start + w - 1) / w : 0;  // (less than an item's cost)
-    const long long end = (len - start + w - 1) / w;
+    // (divisions by constants: the walk is on the path to a CTA's first load)
+    const auto ceil_of = [&](long long x) { return it.two ? (x + kCost2 - 1) / kCost2 : (x + kCost1 - 1) / kCost1; };
+    t0 = start < 0 ? (int)ceil_of(-start) : 0;
+    const long long end = ceil_of(len - start);
     t1 = it.nt < end ? it.nt : (int)end;
 }
 
