@@ -504,6 +504,32 @@ def test_far_pages(isd, P):
     assert got[0][-1].item() < small
 
 
+def test_chunk_rows_past_32_bits(isd):
+    """Rows of q and out past 2^32 bytes and 2^31 elements: the last requests'
+    rows, and their pages, as by a call of their own."""
+    Hq, Hkv, D, P, n, B, last = 32, 8, 128, 16, 120, 4600, 3
+    T, per = n * B, -(-n // P)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn(T, h, D, generator=g, device="cuda", dtype=torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    pools = [torch.zeros(B * per, P, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    table = torch.randperm(B * per, generator=g, device="cuda").to(torch.int32).view(B, per)
+    out, err = torch.zeros(T, Hq * D, dtype=torch.bfloat16, device="cuda"), i32([0])
+    assert out.numel() > 1 << 31
+    d = isd.make_dims(B, 1, Hq, Hkv, D, 1, P, B * per, per)
+    isd.chunk_attention(d, q, k, v, *pools, table, i32([0] * B), i32(np.arange(B + 1) * n), out,
+                        isd.alloc_chunk_workspace(d, T), err)
+    assert int(err.item()) == 0
+    rows = slice(T - last * n, T)
+    tab = table[-last:].cpu().numpy()
+    kp, vp = (O.append(f64(p[table[-last:].long()].flatten(0, 1)) * 0, f64(x[rows]), np.arange(last * per).reshape(last, per),
+                       [0] * last, [n * b for b in range(last + 1)]) for p, x in zip(pools, (k, v)))
+    for p, want in zip(pools, (kp, vp)):
+        assert np.array_equal(f64(p[torch.from_numpy(tab).long().cuda()].flatten(0, 1)), want)
+    want = O.chunk_attention(f64(q[rows]), kp, vp, np.arange(last * per).reshape(last, per).tolist(), [0] * last,
+                             [n * b for b in range(last + 1)], d.sm_scale)
+    check_rows(f64(out[rows]).reshape(last * n, Hq, D), *want, D, n)
+
+
 def test_chunk_refuses_wrong_tensors(isd):
     c = Chunk(isd, 4, 2, 128, 16, [10], [4], seed=16).upload()
     with pytest.raises(ValueError):
