@@ -16,12 +16,18 @@
 //  * the items' 128-key tiles, flattened, are cut into one equal range per CTA
 //    (the lengths are on the device, so every CTA works the cut out itself);
 //  * cached keys come from their pages by TMA, new keys from k_new / v_new
-//    themselves, so nothing waits for the append, which warps do while they
-//    have nothing else;
+//    themselves, so no product waits for the append.  The softmax warps append a
+//    token each at the start, the fixing warp the rest, one by one, while it has
+//    nothing to fix and after its last piece.  Behind enough attention that is
+//    hidden (55 tokens a CTA in the long prompts below); a call of many new tokens
+//    and little attention ends with it (512 prompts of 128 tokens, 443 a CTA: 1.7
+//    ms, where its bytes would take 0.25);
 //  * S = Q.K^T and O += P.V run on the tensor cores with S, P and O in TMEM
 //    (P overwrites S as bf16); a softmax thread owns one row, its maximum and
-//    sum live in registers, and O is rescaled only when a maximum grows by
-//    more than 2^8;
+//    sum live in registers.  Weights are taken by the reference as it stands, an
+//    earlier maximum: O is rescaled only when a row has none yet, when half a
+//    tile's weights sum to more than 2^10, or, in tiles that some row does not
+//    see whole, when the maximum has grown by more than 2^8;
 //  * two warpgroups of softmax threads, each with its S and O, so that one's
 //    softmax runs under the other's products: in an item of two tiles each
 //    has a tile, in an item of one they take the key tiles in turn and add up
@@ -32,11 +38,13 @@
 //    flight are drained and TMEM is released.
 //
 // Measured with 32 / 8 heads of 128: four prompts of 2 k tokens behind 4 to 8 k
-// (885 GFLOP) 785 us, 1.13 PFLOP/s, the tensor core and the exponentials' unit at
-// 0.61 each (a tile's scores, weights and product follow one another in each of
-// the two warpgroups: 3.3 thousand cycles for 2 x 1024 of either); 32 requests of
-// one token behind 512 to 8192 (621 MB) 115 us, 5.4 TB/s, memory; one token
-// behind 1000 tokens 13 us and 3.4 for the join, nearly all of it latency.
+// (885 GFLOP) 785 to 820 us in one launch, cool, 1.08 to 1.13 PFLOP/s, and 965 call
+// after call at the power cap, 0.92; the tensor core and the exponentials' unit
+// are at 0.58 to 0.61 each (a tile's scores, weights and product follow one
+// another in each of the two warpgroups: 3.3 thousand cycles for 2 x 1024 of
+// either).  32 requests of one token behind 512 to 8192 (621 MB) 115 to 120 us,
+// 5.2 to 5.4 TB/s, memory; one token behind 1000 tokens 13.5 us and 3.4 for the
+// join, nearly all of it latency.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -75,7 +83,7 @@ struct ChunkCut {
 struct ChunkArgs : CutShape {
     int B, T, Hq, Hkv, grp, box, num_pages;
     int tps;        // tokens of a tile of 32 rows
-    int grouped;    // layout of a cached tile (see kGroup)
+    int grouped;    // layout of a cached tile (see kGroupRows)
     int part_rows;  // rows of a partial result
     float scale_log2;
     const int32_t* page_table;
@@ -996,7 +1004,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const int step = p.mode == kTwo ? 1 : 2, t_first = p.t0 + (p.mode == kTwo ? 0 : wg);
             float m_ref = -INFINITY, l = 0.f;
             // the row's maximum is top: the reference, l, and O if it holds products,
-            // follow (the maximum's own weight is then 1, which bf16 holds exactly)
+            // follow.  (The maximum's own weight is then 1 but for the reference's
+            // rounding, half a step of its 32 bits: 1 +- 1.7e-4 at references of 4096
+            // to 8192, which is 1 in bf16.)
             auto move_ref = [&](float top, bool has_o) {
                 const float m_new = fmaxf(m_ref, top);
                 const float f = m_new > m_ref ? ex2(m_ref - m_new) : 1.f;
@@ -1031,12 +1041,16 @@ chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 }
                 return fmaxf(x, y);
             };
-            // weights of 32 scores: rounded to bf16 for the product with V, summed in
-            // 32 bits.  (The special-function unit, 16 exponentials a clock and SM,
-            // is what two warps on a sub-partition wait for here: 522 cycles for 32
-            // scores each, one alone 302.  Taking a part of them by a polynomial on
-            // the FMA pipes, which costs 22 cycles a pair against 16, measured 475 to
-            // 500 at best, and no gain for the whole kernel.)
+            // weights of 32 scores: summed in 32 bits, and rounded to bf16 for the
+            // product with V, whose operands have one type (V's).  A weight is off by
+            // half a bf16 step, 2^-8 of itself: against 64 bits results are off by
+            // 0.0020 to 0.0023 (norm), of which their own rounding is 0.0016; keeping
+            // the weights' low halves too would double the product.  (The
+            // special-function unit, 16 exponentials a clock and SM, is what two warps
+            // on a sub-partition wait for here: 522 cycles for 32 scores each, one alone
+            // 302.  Taking a part of them by a polynomial on the FMA pipes, which costs
+            // 22 cycles a pair against 16, measured 475 to 500 at best, and no gain for
+            // the whole kernel.)
             auto weights = [&](const float (&s)[32], float mu, unsigned long long& sum, uint32_t* w) {
                 const unsigned long long sc = pair(a.scale_log2, a.scale_log2), neg = pair(-mu, -mu);
 #pragma unroll
