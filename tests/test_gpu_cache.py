@@ -8,6 +8,10 @@ once more (2^-8 of itself).  A score is a sum of D fp32 products, off by at most
 much each; sums over the keys are fp32 in chunks of at least 8 (keys / 8 steps
 of 2^-23, and 2^-14 covers the exponential and the merging of partial sums).
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -426,6 +430,74 @@ def test_chunk_graph_and_streams(isd):
             b.call()
     a.check()
     b.check()
+
+
+def test_chunk_captured_behind_copies_and_a_joined_stream(isd):
+    """The kernel may start under the one before it: its inputs come from copies,
+    a memset and another stream's kernels in the same graph, and it runs twice."""
+    c = Chunk(isd, 8, 2, 128, 16, [400, 90, 0], [40, 1, 100], seed=18).upload()
+    state = c.d_in + c.d_pool + c.d_idx
+    keep = [t.clone() for t in state]
+    big = torch.randn(2048, 2048, device="cuda")
+
+    def work():
+        main, side = torch.cuda.current_stream(), torch.cuda.Stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            late = (big @ big)[0, 0] * 0
+            c.d_pool[0].copy_(keep[3] + late.to(torch.bfloat16))
+            c.d_idx[1].copy_(keep[6] + late.int())
+        for t, k in list(zip(state, keep))[:3] + [(state[4], keep[4]), (state[7], keep[7])]:
+            t.copy_(k)
+        c.out.zero_()
+        c.out.add_(7.0)
+        main.wait_stream(side)
+        c.call()
+        c.call()
+
+    work()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        work()
+    for _ in range(10):
+        c.d_in[0].fill_(1.0)
+        c.d_idx[1].fill_(3)
+        g.replay()
+    c.check()
+
+
+FIRST_CALL = """
+import sys, torch
+from speculative_verification_isd_b200 import isd
+i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+bf = lambda *s: torch.randn(*s, device="cuda", dtype=torch.bfloat16)
+d = isd.make_dims(2, 1, 8, 2, 128, 1, 16, 40, 8)
+pools, table, kv, used = [bf(40, 16, 2, 128), bf(40, 16, 2, 128)], i32([list(range(8)), list(range(8, 16))]), i32([20, 50]), i32([2, 4])
+q, k, v, start, out, ws = bf(9, 8, 128), bf(9, 2, 128), bf(9, 2, 128), i32([0, 4, 9]), bf(9, 1024), isd.alloc_chunk_workspace(d, 9)
+new = [i32([0] * 3), i32([0] * 3), torch.empty(3, 8, dtype=torch.int32, device="cuda"), i32([0])]
+par, free, moved, live, pws = i32([0, 0, 1]), i32([16]), torch.empty_like(table), i32([0]), isd.alloc_pages_workspace(d)
+call = {"chunk": lambda: isd.chunk_attention(d, q, k, v, *pools, table, kv, start, out, ws),
+        "fork": lambda: isd.fork_requests(d, par, kv, used, table, free, pools, *new),
+        "compact": lambda: isd.compact_pages(d, table, used, pools, moved, live, pws)}[sys.argv[1]]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    call()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (out, *new, moved, live)]
+call()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (out, *new, moved, live)))
+assert {"chunk": out.isfinite().all(), "fork": new[0].tolist() == [20, 20, 50], "compact": live.item() == 6}[sys.argv[1]]
+"""
+
+
+@pytest.mark.parametrize("what", ["chunk", "fork", "compact"])
+def test_first_call_of_a_process_inside_a_capture(what):
+    subprocess.run([sys.executable, "-c", FIRST_CALL, what], check=True, timeout=120,
+                   cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 
 def test_chunk_call_object_and_larger_workspace(isd):
